@@ -213,8 +213,11 @@ inline mala_status fwd_varlen_bf16(const void* Q, const void* K, const void* V, 
   p.O = reinterpret_cast<__nv_bfloat16*>(O);
   p.LSE = LSE;
   p.scale_log2 = scale * kLog2e;
-  p.never_skip = tau == 0.f;
-  p.log2_tau = tau > 0.f ? log2f(tau) : 0.f;
+  // tau = 0 goes through the ordinary test with a threshold that every tile
+  // passes: never_skip makes the producer load V ahead of the decisions, which
+  // only the DENSE instantiation's softmax warps count on
+  p.never_skip = 0;
+  p.log2_tau = tau > 0.f ? log2f(tau) : -1e30f;
   p.kept_tiles = kept;
   p.keep_bits = bits;
   p.Hq = Hq;
