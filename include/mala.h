@@ -51,7 +51,9 @@ typedef enum {
   MALA_ERR_UNSUPPORTED = 2, /* (dtype, d, tile) combination not built */
   MALA_ERR_CUDA = 3,        /* CUDA runtime error at launch or check */
   MALA_ERR_TIMEOUT = 4,     /* a device-side wait ran out (see mala_check) */
-  MALA_ERR_TOO_LARGE = 5    /* shape needs more than the built-in scratch */
+  MALA_ERR_TOO_LARGE = 5,   /* shape needs more than the built-in scratch */
+  MALA_ERR_BAD_PAGE = 6     /* a paged call met a page or length outside the
+                               cache (found on the device; see mala_check) */
 } mala_status;
 
 typedef enum { MALA_F32 = 0, MALA_BF16 = 1 } mala_dtype;
@@ -257,11 +259,135 @@ mala_status mala_decode_noalloc(const void* q, const void* Kcache,
                                 int32_t* kept_tiles, uint32_t* keep_bits,
                                 void* stream);
 
+/* ------------------------------------------------------------------------
+ * The paged key/value cache in 8 bits
+ *
+ * The pages keep the KV cache whole ("neither compressed nor evicted":
+ * agihunt.info summary, limits paragraph) and say nothing of its storage; this
+ * is an interface choice for serving: sequences grow token by token without
+ * moving, and a key or value takes one byte. Three calls share the cache:
+ * mala_cache_append writes new tokens into it, mala_decode_paged attends over
+ * it, mala_cache_gather reads it back for mala_fwd_varlen.
+ *
+ * A page holds `page_size` tokens of every key/value head. A key is e4m3 *
+ * k_scale[page][head], a value e4m3 * v_scale[page][head]. Position p of
+ * sequence b is row p % page_size of page page_table[b][p / page_size]. A
+ * page may stand in the tables of several sequences (a shared prefix); a page
+ * that a mala_cache_append writes to belongs to one sequence. Table entries past a
+ * sequence's last page are not read.
+ *
+ * All pointers are device pointers: the pools 16-byte aligned, the rest by
+ * their element. The strides are in bytes (the elements are bytes), positive
+ * multiples of 16, the last dimension (d) is contiguous; strides of a
+ * dimension of extent 1 are ignored. num_pages and max_pages >= 1; page_size
+ * 16, 32, 64 or 128; d = 128; max_pages * page_size < 2^31.
+ *
+ * What only the device can see (entries of the table, lengths, offsets) is
+ * checked there before it is used: nothing outside the cache is read or
+ * written, what the call did instead is said with it, and the next mala_check
+ * returns MALA_ERR_BAD_PAGE.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  void* k_pages; /* e4m3 [num_pages][Hkv][page_size][d] by the strides */
+  void* v_pages;
+  float* k_scale; /* [num_pages][Hkv] contiguous */
+  float* v_scale;
+  const int32_t* page_table; /* [sequences][max_pages], rows table_stride apart */
+  int64_t k_stride_page, k_stride_head, k_stride_token;
+  int64_t v_stride_page, v_stride_head, v_stride_token;
+  int64_t table_stride; /* in entries, >= max_pages */
+  int num_pages, page_size, max_pages, Hkv, d;
+} mala_paged_cache;
+
+/*
+ * Appends new tokens to the cache: rotates their keys by position, rounds keys
+ * and values to 8 bits and stores them; rotates their queries (optional).
+ *
+ * Sequence b's new tokens are rows [cu_seqlens[b], cu_seqlens[b+1]) of k, v (and
+ * q); they take positions seq_lens[b] - n_b ... seq_lens[b] - 1 (seq_lens counts
+ * them). cu_seqlens = NULL: one new token per sequence, row b (total = batch).
+ *
+ * Rotation of the first rot_dim dimensions of K and Q at position p, with a_i =
+ * p * inv_freq[i], i < rot_dim / 2:
+ *     x_i, x_j  <-  x_i cos a_i - x_j sin a_i,  x_j cos a_i + x_i sin a_i
+ * with j = i + rot_dim / 2, or, with interleaved = 1, the pairs (2i, 2i + 1).
+ * The angle is formed in float64. rot_dim = 0 leaves keys and queries as they are.
+ *
+ * Rounding: with amax the largest finite magnitude among a page's new keys of a
+ * head, s = the least power of two >= 2^-100 with amax <= 448 s. In a page that
+ * held earlier tokens of the sequence, s is at least the scale it had, and
+ * where that grew the earlier tokens are rounded again. Stored is
+ * e4m3(x / s), to nearest even; infinities and NaN are stored as NaN. Values
+ * likewise. Rows of the page behind the new tokens are left as they were.
+ * (The cache's scales are powers of two as long as only this call writes them.)
+ *
+ * Inputs  k, v: [total][Hkv][d] bf16, q: [total][Hq][d] bf16 or NULL, by their
+ *         token and head strides (in elements, multiples of 8; d contiguous;
+ *         base pointers 16-byte aligned), so that rows of a fused projection can
+ *         be passed as they lie; inv_freq: float32 [rot_dim / 2].
+ * Outputs the cache; q_out: [total][Hq][d] bf16 by its strides (may be q itself).
+ * max_new >= every n_b.
+ * A sequence with n_b > max_new, with rows outside [0, total) or with 0 <
+ * seq_lens[b] < n_b is left untouched, tokens whose page is not in the pool
+ * are left out (both reported); a sequence of length <= 0 (an unused slot of
+ * the batch) is skipped, its rows of q_out too.
+ * Supported: rot_dim % 16 == 0, 0 <= rot_dim <= d, Hq % Hkv == 0, batch <=
+ *            65535, Hkv <= 65535.
+ */
+mala_status mala_cache_append(const mala_paged_cache* cache, const void* k,
+                              int64_t k_token_stride, int64_t k_head_stride,
+                              const void* v, int64_t v_token_stride,
+                              int64_t v_head_stride, const void* q,
+                              int64_t q_token_stride, int64_t q_head_stride,
+                              void* q_out, int64_t q_out_token_stride,
+                              int64_t q_out_head_stride,
+                              const int32_t* cu_seqlens,
+                              const int32_t* seq_lens, int batch, int total,
+                              int max_new, int Hq, const float* inv_freq,
+                              int rot_dim, int interleaved, void* stream);
+
+/*
+ * One decode step over the paged cache, with the rule of mala_decode (128-key
+ * tiles aligned from position 0, newest first, the newest always kept; Lq =
+ * seq_lens[b], which counts the current token; tau = 0 is exact attention).
+ *
+ * Inputs  q: [batch][Hq][d] bf16 contiguous (rotated); seq_lens: [batch] int32.
+ * Output  o: [batch][Hq][d] bf16; zero for a sequence of length <= 0; NaN for
+ *         a sequence with a length above max_seqlen or a page that is not in the
+ *         pool (reported).
+ * max_seqlen: an upper bound of the lengths (<= 0: what the table can hold).
+ * Trace   kept_tiles: [batch][Hkv]; keep_bits: [batch][Hkv][ceil(nt/32)], nt =
+ *         ceil(max_seqlen / 128); with per_head = 1, [batch][Hq] and
+ *         [batch][Hq][ceil(nt/32)].
+ * No workspace. Supported: 1 <= Hq / Hkv <= 8, batch, Hkv <= 65535;
+ * MALA_ERR_TOO_LARGE when the statistics of max_seqlen do not fit in shared
+ * memory.
+ */
+mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q,
+                              void* o, const int32_t* seq_lens, int batch,
+                              int Hq, int max_seqlen, float tau, float scale,
+                              int per_head, int32_t* kept_tiles,
+                              uint32_t* keep_bits, void* stream);
+
+/*
+ * Reads sequences back from the cache as the packed bf16 keys and values that
+ * mala_fwd_varlen takes: positions 0 .. n_b - 1 of sequence b, n_b =
+ * cu_seqlens_k[b+1] - cu_seqlens_k[b], become rows cu_seqlens_k[b] .. of K and
+ * V: [total][Hkv][d] bf16. Rows of a page that is not in the pool become NaN
+ * (reported); a sequence with n_b > max_seqlen or rows outside [0, total) is
+ * left out (reported).
+ * Supported: batch <= 65535.
+ */
+mala_status mala_cache_gather(const mala_paged_cache* cache, void* K, void* V,
+                              const int32_t* cu_seqlens_k, int batch,
+                              int max_seqlen, int total, void* stream);
+
 /*
  * Synchronizes `stream`, then reads and clears this GPU's device status word.
  * Returns MALA_ERR_CUDA if the stream reported an error (or a kernel found
  * its shared memory laid out unusably and did nothing), MALA_ERR_TIMEOUT if a
- * kernel gave up on a wait since the last check, MALA_OK otherwise.
+ * kernel gave up on a wait since the last check, MALA_ERR_BAD_PAGE if a paged
+ * call met a page, length or offset outside its cache, MALA_OK otherwise.
  */
 mala_status mala_check(void* stream);
 

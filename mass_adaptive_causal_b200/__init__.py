@@ -10,6 +10,8 @@ Entry points (same names as the C ABI in ``include/mala.h``):
 * :func:`mala_fwd`    -- forward / prefill: O, LSE
 * :func:`mala_bwd`    -- backward: dQ, dK, dV
 * :func:`mala_decode` -- one decode step over a KV cache: o
+* :class:`PagedCache`, :func:`mala_cache_append`, :func:`mala_decode_paged`,
+  :func:`mala_cache_gather` -- the paged KV cache in 8 bits
 * :func:`mala_check`  -- synchronize and read the device status word
 """
 
@@ -19,6 +21,7 @@ import ctypes
 import os
 
 __all__ = ["mala_fwd", "mala_fwd_varlen", "mala_bwd", "mala_decode", "mala_decode_noalloc", "mala_check",
+           "PagedCache", "mala_cache_append", "mala_decode_paged", "mala_cache_gather",
            "mala_selftest_wait", "MalaError", "lib",
            "LIB_PATH", "MALA_F32", "MALA_BF16", "STATUS"]
 
@@ -27,13 +30,24 @@ LIB_PATH = os.path.join(_HERE, "libmala.so")
 
 MALA_F32, MALA_BF16 = 0, 1
 STATUS = {0: "MALA_OK", 1: "MALA_ERR_INVALID_ARG", 2: "MALA_ERR_UNSUPPORTED",
-          3: "MALA_ERR_CUDA", 4: "MALA_ERR_TIMEOUT", 5: "MALA_ERR_TOO_LARGE"}
+          3: "MALA_ERR_CUDA", 4: "MALA_ERR_TIMEOUT", 5: "MALA_ERR_TOO_LARGE",
+          6: "MALA_ERR_BAD_PAGE"}
 
 
 class MalaError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
         super().__init__(f"{where}: {STATUS.get(code, code)}")
+
+
+class _CacheStruct(ctypes.Structure):
+    """mala_paged_cache of include/mala.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale",
+                                                "page_table")]
+                + [(n, ctypes.c_int64) for n in
+                   ("k_stride_page", "k_stride_head", "k_stride_token", "v_stride_page",
+                    "v_stride_head", "v_stride_token", "table_stride")]
+                + [(n, ctypes.c_int) for n in ("num_pages", "page_size", "max_pages", "Hkv", "d")])
 
 
 _lib = None
@@ -71,6 +85,15 @@ def lib() -> ctypes.CDLL:
         L.mala_decode_noalloc.argtypes = [_vp, _vp, _vp, _vp, ci, ci, ci, ci, ci, cf, cf, _i32p,
                                           _u32p, _vp]
         L.mala_decode_noalloc.restype = ci
+        cl = ctypes.c_int64
+        L.mala_cache_append.argtypes = [_vp, _vp, cl, cl, _vp, cl, cl, _vp, cl, cl, _vp, cl, cl,
+                                        _vp, _vp, ci, ci, ci, ci, _vp, ci, ci, _vp]
+        L.mala_cache_append.restype = ci
+        L.mala_decode_paged.argtypes = [_vp, _vp, _vp, _vp, ci, ci, ci, cf, cf, ci, _i32p, _u32p,
+                                        _vp]
+        L.mala_decode_paged.restype = ci
+        L.mala_cache_gather.argtypes = [_vp, _vp, _vp, _vp, ci, ci, ci, _vp]
+        L.mala_cache_gather.restype = ci
         L.mala_check.argtypes = [_vp]
         L.mala_check.restype = ci
         L.mala_selftest_wait.argtypes = [_vp]
@@ -396,9 +419,265 @@ def mala_decode_noalloc(q, k_cache, v_cache, tau: float = 1.0, scale: float = 0.
     return (o, kept, bits) if trace else o
 
 
+# ---------------------------------------------------------------------------
+# the paged KV cache in 8 bits
+# ---------------------------------------------------------------------------
+def _check_pool(k_pages, v_pages, k_scale, v_scale, page_table):
+    torch = _torch()
+    dev = k_pages.device
+    for t in (k_pages, v_pages):
+        if t.dtype != torch.float8_e4m3fn or t.dim() != 4:
+            raise ValueError("pages must be float8_e4m3fn [num_pages, Hkv, page_size, d]")
+        if t.numel() and t.stride(3) != 1:
+            raise ValueError("a page's rows must be contiguous")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape")
+    n, Hkv, page, d = k_pages.shape
+    if page not in (16, 32, 64, 128) or d != 128:
+        raise ValueError("page_size must be 16, 32, 64 or 128, and d 128")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _buf(t, name, dev, torch.float32, (n, Hkv))
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [sequences, max_pages]")
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        raise ValueError("a page table's rows must be contiguous")
+    if v_pages.device != dev or page_table.device != dev:
+        raise ValueError("every tensor of a cache must be on one device")
+    if n < 1 or Hkv < 1 or page_table.shape[0] < 1 or page_table.shape[1] < 1:
+        raise ValueError("the pool and the page table must not be empty")
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        for extent, stride in zip(t.shape[:3], t.stride()[:3]):
+            if extent > 1 and (stride < d or stride % 16):
+                raise ValueError(f"{name}'s strides must be multiples of 16 bytes, at least d")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must be 16-byte aligned")
+
+
+class PagedCache:
+    """A paged KV cache in 8 bits, as the calls below take it.
+
+    k_pages, v_pages: float8_e4m3fn [num_pages, Hkv, page_size, 128] (page_size 16,
+    32, 64 or 128; views such as ``pool[:, 0]`` or a transposed [num_pages, page_size,
+    Hkv, 128] pool will do, as long as the last dimension is contiguous); k_scale,
+    v_scale: float32 [num_pages, Hkv]; page_table: int32 [sequences, max_pages]. Position
+    p of sequence b is row p % page_size of page page_table[b, p // page_size]. A page's
+    memory and scale need no initialization.
+
+    The object holds on to the tensors; their contents (the page table's too) may be
+    changed between calls, the tensors themselves may not be exchanged or resized."""
+
+    __slots__ = ("_tensors", "_struct", "_ref", "_device", "_index", "Hkv", "page_size",
+                 "max_seqlen", "sequences")
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale, page_table):
+        _check_pool(k_pages, v_pages, k_scale, v_scale, page_table)
+        n, Hkv, page, d = k_pages.shape
+        self._tensors = (k_pages, v_pages, k_scale, v_scale, page_table)
+        self._device = k_pages.device
+        self._index = self._device.index
+        self.Hkv, self.page_size = Hkv, page
+        self.sequences, max_pages = page_table.shape
+        self.max_seqlen = max_pages * page
+        stride = page_table.stride(0) if self.sequences > 1 else max_pages
+        if stride < max_pages:
+            raise ValueError("a page table's rows must not overlap")
+        self._struct = _CacheStruct(*(t.data_ptr() for t in self._tensors),
+                                    *k_pages.stride()[:3], *v_pages.stride()[:3], stride,
+                                    n, page, max_pages, Hkv, d)
+        self._ref = ctypes.addressof(self._struct)
+
+    k_pages = property(lambda self: self._tensors[0])
+    v_pages = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+    page_table = property(lambda self: self._tensors[4])
+
+
+def _paged_ready(cache, require_cuda=True):
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    if require_cuda:
+        if cache._device.type != "cuda":
+            raise ValueError("the cache must be on a CUDA device")
+        if cache._index != _torch().cuda.current_device():
+            raise ValueError(f"the cache is on {cache._device}, not on the current CUDA device "
+                             "(torch.cuda.set_device)")
+
+
+def _paged_stream(stream, index):
+    """The stream's handle as a plain number (the current stream of device ``index`` when
+    None), without building a stream object: a decode step's host time counts."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(index)
+
+
+def _check_lens(cache, t, name, n=None):
+    torch = _torch()
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
+    if t.device != cache._device:
+        raise ValueError(f"{name} must be on {cache._device}")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} must hold {n} entries, got {t.shape[0]}")
+
+
+def _check_batch(cache, batch):
+    if batch < 1 or batch > cache.sequences:
+        raise ValueError(f"the batch ({batch}) must be between 1 and the page table's "
+                         f"{cache.sequences} rows")
+
+
+def _rows(cache, t, name, total, heads):
+    """bf16 [total, heads, 128] with rows that may lie apart: (pointer, token stride,
+    head stride)."""
+    torch = _torch()
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.device != cache._device:
+        raise ValueError(f"{name} must be a bf16 [tokens, heads, d] tensor on {cache._device}")
+    if t.shape[0] != total or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must have shape ({total}, {heads or 'heads'}, 128), got "
+                         f"{tuple(t.shape)}")
+    ts, hs, ds = t.stride()
+    if t.shape[0] == 1:
+        ts = 0
+    if t.shape[1] == 1:
+        hs = 0
+    ptr = t.data_ptr()
+    if total and (ds != 1 or ts % 8 or hs % 8 or ptr % 16):
+        raise ValueError(f"{name}: d must be contiguous, the strides multiples of 8 elements and "
+                         "the start 16-byte aligned")
+    return ptr, ts, hs
+
+
+def mala_cache_append(cache, k, v, seq_lens, cu_seqlens=None, max_new: int | None = None,
+                      inv_freq=None, interleaved: bool = False, q=None, q_out=None, stream=None):
+    """Appends new tokens to a PagedCache: keys rotated by position and rounded to 8
+    bits with their page's scale, values rounded; queries rotated.
+
+    k, v: [total, Hkv, 128] bf16, q (optional): [total, Hq, 128] bf16 (rows may lie apart,
+    as in views of a fused projection); seq_lens: int32 [batch], each sequence's
+    length with its new tokens; cu_seqlens: int32 [batch + 1], sequence b's new tokens
+    are rows cu_seqlens[b] .. cu_seqlens[b+1] (None: one new token each); max_new: an upper
+    bound of the new tokens of a sequence (default total, or 1); inv_freq: float32
+    [rot_dim / 2], rot_dim a multiple of 16 (None: no rotation); interleaved: pairs (2i, 2i+1)
+    instead of (i, i + rot_dim / 2). Returns q rotated (q_out, which may be q; a new
+    tensor if None), or None without q."""
+    torch = _torch()
+    _paged_ready(cache)
+    total = k.shape[0]
+    _check_lens(cache, seq_lens, "seq_lens")
+    batch = seq_lens.shape[0]
+    _check_batch(cache, batch)
+    if cu_seqlens is None:
+        if total != batch:
+            raise ValueError("without cu_seqlens every sequence has one new token")
+        max_new = 1
+    else:
+        _check_lens(cache, cu_seqlens, "cu_seqlens", batch + 1)
+        max_new = total if max_new is None else int(max_new)
+        if max_new < 0:
+            raise ValueError("max_new must not be negative")
+    kr = _rows(cache, k, "k", total, cache.Hkv)
+    vr = _rows(cache, v, "v", total, cache.Hkv)
+    qr = qo = (None, 0, 0)
+    Hq = 0
+    if q is not None:
+        qr = _rows(cache, q, "q", total, None)
+        Hq = q.shape[1]
+        if Hq < 1 or Hq % cache.Hkv:
+            raise ValueError("the query heads must be a multiple of the key/value heads")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qo = _rows(cache, q_out, "q_out", total, Hq)
+        if qo[0] == qr[0] and qo != qr:
+            raise ValueError("q_out may be q itself, or must not overlap it")
+        if total > 1 and qo[1] == 0 or Hq > 1 and qo[2] == 0:
+            raise ValueError("q_out's rows must not overlap")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot, freq = 0, None
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() \
+                or inv_freq.device != cache._device:
+            raise ValueError(f"inv_freq must be a contiguous 1-D float32 tensor on {cache._device}")
+        rot = 2 * inv_freq.shape[0]
+        if rot % 16 or rot > 128:
+            raise ValueError("rot_dim = 2 * len(inv_freq) must be a multiple of 16, at most d")
+        freq = inv_freq.data_ptr() if rot else None
+    code = lib().mala_cache_append(cache._ref, *kr, *vr, *qr, *qo,
+                                   None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                                   seq_lens.data_ptr(), batch, total, max_new, Hq, freq, rot,
+                                   int(bool(interleaved)), _paged_stream(stream, cache._index))
+    _raise(code, "mala_cache_append")
+    return q_out
+
+
+def mala_decode_paged(q, cache, seq_lens, tau: float = 1.0, scale: float = 0.0,
+                      per_head: bool = False, max_seqlen: int | None = None, trace: bool = False,
+                      out=None, stream=None):
+    """One decode step over a PagedCache, with the rule of mala_decode. q: [batch, Hq,
+    128] bf16 (rotated); seq_lens: int32 [batch], the current token included (0: an
+    unused slot, its output is zero); max_seqlen: an upper bound of the lengths (default:
+    what the page table can hold). Returns o like q or, with ``trace=True``, (o, kept_tiles
+    [batch, Hkv], keep_bits [batch, Hkv, nw]), per query head with ``per_head=True``;
+    nw covers max_seqlen."""
+    torch = _torch()
+    _paged_ready(cache)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous() \
+            or q.device != cache._device:
+        raise ValueError(f"q must be a contiguous bf16 [batch, Hq, 128] tensor on {cache._device}")
+    batch, Hq, _ = q.shape
+    _check_batch(cache, batch)
+    if Hq < 1 or Hq % cache.Hkv:
+        raise ValueError("the query heads must be a multiple of the key/value heads")
+    _check_lens(cache, seq_lens, "seq_lens", batch)
+    limit = cache.max_seqlen if max_seqlen is None else int(max_seqlen)
+    if limit < 1:
+        raise ValueError("max_seqlen must be positive")
+    o = torch.empty_like(q) if out is None else _buf(out, "out", cache._device, q.dtype, q.shape)
+    kept = bits = None
+    if trace:
+        rows = Hq if per_head else cache.Hkv
+        kept = torch.empty((batch, rows), dtype=torch.int32, device=q.device)
+        bits = torch.empty((batch, rows, (n_blocks(limit, 128) + 31) // 32), dtype=torch.int32,
+                           device=q.device)
+    code = lib().mala_decode_paged(cache._ref, q.data_ptr(), o.data_ptr(), seq_lens.data_ptr(),
+                                   batch, Hq, limit, float(tau), float(scale),
+                                   int(bool(per_head)), _ptr(kept), _ptr(bits), _paged_stream(stream, cache._index))
+    _raise(code, "mala_decode_paged")
+    return (o, kept, bits) if trace else o
+
+
+def mala_cache_gather(cache, cu_seqlens_k, max_seqlen: int, total: int, out=None, stream=None):
+    """Reads sequences of a PagedCache back as packed bf16 (K, V), [total, Hkv, 128]
+    each, the form mala_fwd_varlen takes: positions 0 .. n_b - 1 of sequence b, n_b =
+    cu_seqlens_k[b+1] - cu_seqlens_k[b] <= max_seqlen. ``out``: a (K, V) pair to fill."""
+    torch = _torch()
+    _paged_ready(cache)
+    _check_lens(cache, cu_seqlens_k, "cu_seqlens_k")
+    batch = cu_seqlens_k.shape[0] - 1
+    _check_batch(cache, batch)
+    total, max_seqlen = int(total), int(max_seqlen)
+    if total < 0 or max_seqlen < 0:
+        raise ValueError("total and max_seqlen must not be negative")
+    shape = (total, cache.Hkv, 128)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=cache._device)
+                    for _ in range(2))
+    k, v = out
+    _buf(k, "K", cache._device, torch.bfloat16, shape)
+    _buf(v, "V", cache._device, torch.bfloat16, shape)
+    code = lib().mala_cache_gather(cache._ref, k.data_ptr(), v.data_ptr(),
+                                   cu_seqlens_k.data_ptr(), batch, max_seqlen, total,
+                                   _paged_stream(stream, cache._index))
+    _raise(code, "mala_cache_gather")
+    return k, v
+
+
 def mala_check(stream=None):
     """Synchronize the stream and raise MalaError if a kernel reported a
-    timeout or the stream holds a CUDA error."""
+    timeout, a paged call met a page, length or offset outside its cache, or the
+    stream holds a CUDA error."""
     _raise(lib().mala_check(_stream(stream)), "mala_check")
 
 

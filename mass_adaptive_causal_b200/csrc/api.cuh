@@ -531,6 +531,7 @@ const char* mala_status_string(mala_status s) {
     case MALA_ERR_CUDA: return "MALA_ERR_CUDA";
     case MALA_ERR_TIMEOUT: return "MALA_ERR_TIMEOUT";
     case MALA_ERR_TOO_LARGE: return "MALA_ERR_TOO_LARGE";
+    case MALA_ERR_BAD_PAGE: return "MALA_ERR_BAD_PAGE";
   }
   return "MALA_ERR_UNKNOWN";
 }
@@ -679,7 +680,8 @@ mala_status mala_check(void* stream) {
   if (st != 0) {
     if (cudaMemcpyToSymbol(mala::g_status, &zero, sizeof(zero)) != cudaSuccess)
       return MALA_ERR_CUDA;
-    return (st & mala::kStatusTimeout) ? MALA_ERR_TIMEOUT : MALA_ERR_CUDA;
+    if (st & mala::kStatusTimeout) return MALA_ERR_TIMEOUT;
+    return st == mala::kStatusPage ? MALA_ERR_BAD_PAGE : MALA_ERR_CUDA;
   }
   return MALA_OK;
 }

@@ -1,0 +1,187 @@
+// api_paged.cuh -- the C entry points of the paged 8-bit cache: argument
+// checks and launches (the contract is in include/mala.h).
+#pragma once
+
+#include "api.cuh"
+#include "decode_paged_sm100.cuh"
+#include "paged.cuh"
+
+namespace mala {
+namespace host {
+
+constexpr long long kMaxPositions = 0x7fffffffll - 256;
+
+// Checks the cache's description and turns it into the kernels' view.
+inline mala_status make_pool(const mala_paged_cache* c, paged::Pool* p) {
+  if (!c) return MALA_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->max_pages < 1 || c->Hkv < 1 || c->Hkv > 65535)
+    return MALA_ERR_INVALID_ARG;
+  if (c->d != paged::D || (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 &&
+                           c->page_size != 128))
+    return MALA_ERR_UNSUPPORTED;
+  if ((long long)c->max_pages * c->page_size > kMaxPositions) return MALA_ERR_INVALID_ARG;
+  if (!c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->page_table)
+    return MALA_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return MALA_ERR_INVALID_ARG;
+  const void* words[] = {c->k_scale, c->v_scale, c->page_table};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return MALA_ERR_INVALID_ARG;
+  const int64_t strides[] = {c->k_stride_page, c->k_stride_head, c->k_stride_token,
+                             c->v_stride_page, c->v_stride_head, c->v_stride_token};
+  const int extent[] = {c->num_pages, c->Hkv, c->page_size};
+  for (int i = 0; i < 6; ++i)
+    if (extent[i % 3] > 1 &&
+        (strides[i] < paged::D || (strides[i] & 15) || strides[i] >= (1ll << 40)))
+      return MALA_ERR_INVALID_ARG;
+  if (c->table_stride < c->max_pages) return MALA_ERR_INVALID_ARG;
+  p->k = reinterpret_cast<uint8_t*>(c->k_pages);
+  p->v = reinterpret_cast<uint8_t*>(c->v_pages);
+  p->k_scale = c->k_scale;
+  p->v_scale = c->v_scale;
+  p->table = c->page_table;
+  p->k_page = c->k_stride_page;
+  p->k_head = c->k_stride_head;
+  p->k_tok = c->k_stride_token;
+  p->v_page = c->v_stride_page;
+  p->v_head = c->v_stride_head;
+  p->v_tok = c->v_stride_token;
+  p->table_stride = c->table_stride;
+  p->num_pages = c->num_pages;
+  p->page = c->page_size;
+  p->max_pages = c->max_pages;
+  p->Hkv = c->Hkv;
+  return MALA_OK;
+}
+
+// An input or output of append: [total][heads][128] bf16 by its strides.
+inline bool rows_ok(const void* ptr, int64_t token_stride, int64_t head_stride) {
+  return ptr && aligned16(ptr) && !(token_stride & 7) && !(head_stride & 7);
+}
+
+}  // namespace host
+}  // namespace mala
+
+extern "C" {
+
+mala_status mala_cache_append(const mala_paged_cache* cache, const void* k, int64_t k_token_stride,
+                              int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                              int64_t v_head_stride, const void* q, int64_t q_token_stride,
+                              int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
+                              int64_t q_out_head_stride, const int32_t* cu_seqlens,
+                              const int32_t* seq_lens, int batch, int total, int max_new, int Hq,
+                              const float* inv_freq, int rot_dim, int interleaved, void* stream) {
+  mala::paged::AppendParams p = {};
+  const mala_status st = make_pool(cache, &p.pool);
+  if (st != MALA_OK) return st;
+  const int Hkv = cache->Hkv;
+  if (batch < 1 || total < 0 || max_new < 0 || (interleaved != 0 && interleaved != 1))
+    return MALA_ERR_INVALID_ARG;
+  if (batch > 65535 || (q && (Hq < 1 || Hq % Hkv != 0))) return MALA_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > mala::paged::D || rot_dim % 16 != 0) return MALA_ERR_UNSUPPORTED;
+  if (!cu_seqlens && total != batch) return MALA_ERR_INVALID_ARG;
+  if (!seq_lens || (rot_dim > 0 && !inv_freq)) return MALA_ERR_INVALID_ARG;
+  const void* words[] = {cu_seqlens, seq_lens, inv_freq};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return MALA_ERR_INVALID_ARG;
+  if (total == 0 || max_new == 0) return MALA_OK;
+  if (!rows_ok(k, k_token_stride, k_head_stride) || !rows_ok(v, v_token_stride, v_head_stride))
+    return MALA_ERR_INVALID_ARG;
+  if (q && (!rows_ok(q, q_token_stride, q_head_stride) ||
+            !rows_ok(q_out, q_out_token_stride, q_out_head_stride)))
+    return MALA_ERR_INVALID_ARG;
+  p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  p.k_tok = k_token_stride;
+  p.k_head = k_head_stride;
+  p.v_tok = v_token_stride;
+  p.v_head = v_head_stride;
+  p.q_tok = q_token_stride;
+  p.q_head = q_head_stride;
+  p.qo_tok = q_out_token_stride;
+  p.qo_head = q_out_head_stride;
+  p.cu = cu_seqlens;
+  p.seq_lens = seq_lens;
+  p.inv_freq = inv_freq;
+  p.rot = rot_dim;
+  p.interleaved = interleaved;
+  p.G = q ? Hq / Hkv : 0;
+  p.total = total;
+  p.max_new = max_new < total ? max_new : total;
+  const int page = cache->page_size;
+  // n consecutive positions lie in at most (n + page - 2) / page + 1 pages
+  const dim3 grid((unsigned)(((long long)p.max_new + page - 2) / page + 1), batch, Hkv);
+  cudaStream_t s = as_stream(stream);
+  if (page <= 32)
+    mala::paged::append_kernel<1><<<grid, mala::paged::APPEND_NT, 0, s>>>(p);
+  else if (page == 64)
+    mala::paged::append_kernel<2><<<grid, mala::paged::APPEND_NT, 0, s>>>(p);
+  else
+    mala::paged::append_kernel<4><<<grid, mala::paged::APPEND_NT, 0, s>>>(p);
+  return launch_status();
+}
+
+mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q, void* o,
+                              const int32_t* seq_lens, int batch, int Hq, int max_seqlen,
+                              float tau, float scale, int per_head, int32_t* kept_tiles,
+                              uint32_t* keep_bits, void* stream) {
+  mala::pdec::Params p = {};
+  const mala_status st = make_pool(cache, &p.pool);
+  if (st != MALA_OK) return st;
+  const int Hkv = cache->Hkv;
+  if (batch < 1 || batch > 65535 || Hq < 1 || Hq % Hkv != 0) return MALA_ERR_INVALID_ARG;
+  if (per_head != 0 && per_head != 1) return MALA_ERR_INVALID_ARG;
+  if (!tau_ok(tau)) return MALA_ERR_INVALID_ARG;
+  if (Hq / Hkv > mala::pdec::GMAX) return MALA_ERR_UNSUPPORTED;
+  if (!q || !o || !seq_lens || !aligned16(q) || !aligned16(o)) return MALA_ERR_INVALID_ARG;
+  const void* words[] = {seq_lens, kept_tiles, keep_bits};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return MALA_ERR_INVALID_ARG;
+  const int held = cache->max_pages * cache->page_size;
+  if (max_seqlen <= 0) max_seqlen = held;
+  const int nt = (int)(((long long)max_seqlen + 127) / 128);
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.o = reinterpret_cast<__nv_bfloat16*>(o);
+  p.seq_lens = seq_lens;
+  p.G = Hq / Hkv;
+  p.Hkv = Hkv;
+  p.nw = (nt + 31) / 32;  // trace rows are laid out by the caller's max_seqlen
+  p.max_tiles = nt < (held + 127) / 128 ? nt : (held + 127) / 128;
+  p.scale_log2 = resolve_scale(scale, mala::paged::D) * mala::kLog2e;
+  p.never_skip = tau == 0.f;
+  p.log2_tau = tau > 0.f ? log2f(tau) : 0.f;
+  p.per_head = per_head;
+  p.kept_tiles = kept_tiles;
+  p.keep_bits = keep_bits;
+  const size_t smem = mala::pdec::smem_bytes(p.G, p.max_tiles);
+  if (smem > 220 * 1024) return MALA_ERR_TOO_LARGE;
+  MALA_CUDA_TRY(cudaFuncSetAttribute(mala::pdec::decode_kernel,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  mala::pdec::decode_kernel<<<dim3(Hkv, batch), mala::pdec::NT, smem, as_stream(stream)>>>(p);
+  return launch_status();
+}
+
+mala_status mala_cache_gather(const mala_paged_cache* cache, void* K, void* V,
+                              const int32_t* cu_seqlens_k, int batch, int max_seqlen, int total,
+                              void* stream) {
+  mala::paged::GatherParams p = {};
+  const mala_status st = make_pool(cache, &p.pool);
+  if (st != MALA_OK) return st;
+  if (batch < 1 || batch > 65535 || total < 0 || max_seqlen < 0) return MALA_ERR_INVALID_ARG;
+  if (!cu_seqlens_k || (reinterpret_cast<uintptr_t>(cu_seqlens_k) & 3u))
+    return MALA_ERR_INVALID_ARG;
+  if (total == 0 || max_seqlen == 0) return MALA_OK;
+  if (!K || !V || !aligned16(K) || !aligned16(V)) return MALA_ERR_INVALID_ARG;
+  p.k = reinterpret_cast<__nv_bfloat16*>(K);
+  p.v = reinterpret_cast<__nv_bfloat16*>(V);
+  p.cu = cu_seqlens_k;
+  p.total = total;
+  p.max_seqlen = max_seqlen < total ? max_seqlen : total;
+  const int page = cache->page_size;
+  const dim3 grid((p.max_seqlen - 1) / page + 1, batch);
+  mala::paged::gather_kernel<<<grid, mala::paged::GATHER_NT, 0, as_stream(stream)>>>(p);
+  return launch_status();
+}
+
+}  // extern "C"

@@ -6,6 +6,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -21,6 +22,7 @@ __device__ unsigned int g_status_where = 0;
 enum : unsigned int {
   kStatusTimeout = 1u,
   kStatusLayout = 2u,  // a kernel found its dynamic shared memory misaligned
+  kStatusPage = 4u,    // a page table entry, or a length, outside the paged cache
 };
 
 // Wait limit for every device-side spin: about two seconds of %globaltimer.
@@ -38,6 +40,10 @@ __device__ __forceinline__ void record_timeout(unsigned int where) {
 }
 __device__ __forceinline__ void record_layout_error(unsigned int where) {
   atomicOr(&g_status, kStatusLayout);
+  atomicExch(&g_status_where, where);
+}
+__device__ __forceinline__ void record_bad_page(unsigned int where) {
+  atomicOr(&g_status, kStatusPage);
   atomicExch(&g_status_where, where);
 }
 

@@ -2,6 +2,7 @@
 // device status word (common.cuh) exists once per GPU and every kernel can
 // set it without relocatable device code.
 #include "api.cuh"
+#include "api_paged.cuh"
 
 // -------------------------------------------------------------------------
 // mala_decode_noalloc: the decode step with its workspace in a static device

@@ -1,0 +1,629 @@
+"""The paged 8-bit cache on the GPU: append, decode and gather against float64
+(tests/paged_ref.py, and the oracle for the decode rule), at the sizes, masks, strides
+and contents where they can go wrong, and used together. The bounds are derived in
+tests/paged_ref.py."""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from tests import paged_ref as R
+from tests.parity import as_f64, compare_decode_keep, rel_l2
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import mass_adaptive_causal_b200 as mala  # noqa: E402
+
+f8, bf16, i32 = torch.float8_e4m3fn, torch.bfloat16, torch.int32
+LAYOUTS = ["plain", "token_major", "interleaved_kv"]
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def new_pool(n, Hkv, page, layout="plain"):
+    """k, v pages full of NaN bytes (as memory that nothing has written may be), scales NaN."""
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    if layout == "plain":
+        k, v = (torch.full((n, Hkv, page, 128), 0x7f, **u8) for _ in range(2))
+    elif layout == "token_major":
+        k, v = (torch.full((n, page, Hkv, 128), 0x7f, **u8).transpose(1, 2) for _ in range(2))
+    else:
+        both = torch.full((n, 2, Hkv, page, 128), 0xff, **u8)
+        k, v = both[:, 0], both[:, 1]
+    s = torch.full((2, n, Hkv), float("nan"), device="cuda")
+    return k.view(f8), v.view(f8), s[0].contiguous(), s[1].contiguous()
+
+
+def table_for(lens, page, n_pages, g, spare=2):
+    """Pages from all over the pool; entries past a sequence's last page are no pages."""
+    width = max(-(-n // page) for n in lens) + spare
+    order = torch.randperm(n_pages, device="cuda", generator=g).int()
+    t = torch.empty((len(lens), width + 3), dtype=i32, device="cuda")[:, :width]
+    t[:, 0::2], t[:, 1::2] = -7, 1 << 30
+    at = 0
+    for b, n in enumerate(lens):
+        m = -(-n // page)
+        t[b, :m] = order[at:at + m]
+        at += m
+    return t
+
+
+def pages_needed(lens, page):
+    return sum(-(-n // page) for n in lens)
+
+
+def filled(lens, Hkv, page, layout, seed, peak=True, pow2=True):
+    """A cache with content for sequences of these lengths; rows behind a sequence stay NaN."""
+    g = gen(seed)
+    n_pages = pages_needed(lens, page) + 3
+    k, v, ks, vs = new_pool(n_pages, Hkv, page, layout)
+    t = table_for(lens, page, n_pages, g)
+    for b, n in enumerate(lens):
+        for s in range(-(-n // page)):
+            pid, rows = int(t[b, s]), min(page, n - s * page)
+            x = torch.randn((2, Hkv, rows, 128), device="cuda", generator=g).clamp(-4, 4) * 100
+            k.view(torch.uint8)[pid, :, :rows] = x[0].to(f8).view(torch.uint8)
+            v.view(torch.uint8)[pid, :, :rows] = x[1].to(f8).view(torch.uint8)
+        ids = t[b, :-(-n // page)].long()
+        e = torch.randint(-9, -4, (2, len(ids), Hkv), device="cuda", generator=g)
+        if peak:  # a few pages with much larger or smaller values
+            e += 6 * (torch.rand(e.shape, device="cuda", generator=g) < 0.1).long()
+        sc = torch.exp2(e.float())
+        if not pow2:
+            sc *= 1 + torch.rand(e.shape, device="cuda", generator=g)
+        ks[ids], vs[ids] = sc[0], sc[1] * 8
+    return k, v, ks, vs, t
+
+
+def check_decode(tensors, lens, q, o, tau, per_head, kept=None, bits=None, skip=()):
+    k, v, ks, vs, t = tensors
+    Hkv, G = k.shape[1], q.shape[1] // k.shape[1]
+    qn, on = as_f64(q), as_f64(o)
+    compared = 0
+    for b, n in enumerate(lens):
+        if b in skip:
+            continue
+        if n <= 0:
+            assert (on[b] == 0).all() and (kept is None or int(kept[b].abs().sum()) == 0)
+            assert bits is None or int(bits[b].abs().sum()) == 0
+            continue
+        K, V = R.sequence((k, v, ks, vs), t, b, n)
+        ref = oracle.decode(qn[b], K, V, tau=tau, per_head=per_head, want_margin=True)
+        nt = oracle.n_blocks(n, 128)
+        for h in range(q.shape[1]):
+            unit = h if per_head else h // G
+            if bits is not None:
+                gk = mala.unpack_bits(bits[b], 32 * bits.shape[2])[unit]
+                assert not gk[nt:].any()
+                if compare_decode_keep(gk[:nt], ref["keep"][unit], ref["margin"][unit]):
+                    continue
+                assert int(kept[b, unit]) == int(ref["keep"][unit].sum())
+            keys = np.repeat(ref["keep"][unit].astype(bool), 128)[:n]
+            tol = R.decode_bound(qn[b, h], K[h // G], V[h // G], ref["o"][h], keys)
+            assert (np.abs(on[b, h] - ref["o"][h]) <= tol).all(), (b, h, n)
+            compared += 1
+    return compared
+
+
+# ---------------------------------------------------------------------------- decode
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_decode_lengths_and_layouts(page, layout):
+    lens = [1, 0, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 500, 1000, 2049]
+    Hkv, G = 2, 4
+    tensors = filled(lens, Hkv, page, layout, 100 + page)
+    q = (torch.randn((len(lens), Hkv * G, 128), device="cuda", generator=gen(1)) * 0.5).to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    for tau in (1.0, 0.0):
+        o, kept, bits = mala.mala_decode_paged(q, cache, sl, tau=tau, trace=True)
+        mala.mala_check()
+        assert check_decode(tensors, lens, q, o, tau, False, kept, bits) >= 0.9 * 18 * Hkv * G
+
+
+@pytest.mark.parametrize("G", range(1, 9))
+@pytest.mark.parametrize("per_head", [False, True])
+def test_decode_groups(G, per_head):
+    lens = [700, 129, 3000]
+    Hkv = 3
+    tensors = filled(lens, Hkv, 32, "plain", 200 + G, pow2=False)
+    q = torch.randn((3, Hkv * G, 128), device="cuda", generator=gen(G)).to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    for tau in (1.0, 0.05):
+        o, kept, bits = mala.mala_decode_paged(q, cache, sl, tau=tau, per_head=per_head, trace=True)
+        mala.mala_check()
+        assert check_decode(tensors, lens, q, o, tau, per_head, kept, bits) >= 0.9 * 9 * G
+
+
+@pytest.mark.parametrize("B,Hkv,n,tau", [(1, 1, 40000, 1.0), (1, 8, 9000, 1.0), (2, 1, 70001, 0.0),
+                                          (40, 2, 3000, 1.0), (3, 2, 20000, 1e-4)])
+def test_decode_long_and_many(B, Hkv, n, tau):
+    """Few and many groups, long contexts: however the work is split. Keys of the sequence's
+    own query stand out, so that tiles are kept here and there."""
+    g = gen(n)
+    lens = [n - 37 * i for i in range(B)]
+    page = 64
+    tensors = filled(lens, Hkv, page, "plain", n, peak=False)
+    k, v, ks, vs, t = tensors
+    G = 4
+    q = (torch.randn((B, Hkv * G, 128), device="cuda", generator=g) * 0.4).to(bf16)
+    for b, m in enumerate(lens):
+        for pos in torch.randint(0, m, (9,), generator=g, device="cuda").tolist():
+            pid = int(t[b, pos // page])
+            x = q[b].float().view(Hkv, G, 128)[:, pos % G]
+            k.view(torch.uint8)[pid, :, pos % page] = (x * 400).clamp(-448, 448).to(f8).view(torch.uint8)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    o, kept, bits = mala.mala_decode_paged(q, cache, sl, tau=tau, trace=True)
+    mala.mala_check()
+    pick = sorted(set([0, B // 2, B - 1]))
+    for b in pick:
+        assert check_decode((k, v, ks, vs, t[b:b + 1]), [lens[b]], q[b:b + 1], o[b:b + 1], tau,
+                            False, kept[b:b + 1], bits[b:b + 1]) >= 0.7 * Hkv * G
+
+
+def test_decode_max_seqlen_bounds_and_odd_values():
+    """Looser and exact bounds of the length give the same answer; explicit scale; q = 0; one key
+    that takes all the mass; scores far apart; a large q."""
+    lens = [300, 300, 300, 300, 1]
+    tensors = filled(lens, 2, 16, "plain", 7)
+    k = tensors[0]
+    q = torch.randn((5, 6, 128), device="cuda", generator=gen(3))
+    q[0] = 0
+    q[1] *= 1e4
+    q[2] *= 1e-30
+    q = q.to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    a = mala.mala_decode_paged(q, cache, sl, tau=1.0)
+    b = mala.mala_decode_paged(q, cache, sl, tau=1.0, max_seqlen=300)
+    out = torch.empty_like(q)
+    assert mala.mala_decode_paged(q, cache, sl, tau=1.0, max_seqlen=100000, out=out) is out
+    c = mala.mala_decode_paged(q, cache, sl, tau=1.0, scale=1 / math.sqrt(128))
+    mala.mala_check()
+    assert torch.equal(out, a) or rel_l2(as_f64(out), as_f64(a)) < 2e-3
+    assert rel_l2(as_f64(b), as_f64(a)) < 2e-3 and torch.equal(c, a)
+    check_decode(tensors, lens, q, a, 1.0, False, skip=(1,))
+    # q = 1e4 * N(0, 1): one key has all the mass, to within exp(-100)
+    K, V = R.sequence(tensors[:4], tensors[4], 1, 300)
+    qn, on = as_f64(q), as_f64(a)
+    for h in range(6):
+        s = K[h // 3] @ qn[1, h] / math.sqrt(128)
+        top = np.sort(s)[-2:]
+        if top[1] - top[0] > 100:
+            assert (np.abs(on[1, h] - V[h // 3][s.argmax()]) <= 2.0 ** -8 * np.abs(on[1, h])).all()
+
+
+def test_decode_nan_stays_in_its_head_and_shows():
+    lens = [400, 400]
+    tensors = filled(lens, 2, 64, "plain", 11)
+    k, v, ks, vs, t = tensors
+    q = (torch.randn((2, 4, 128), device="cuda", generator=gen(5)) * 0.3).to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    clean = mala.mala_decode_paged(q, cache, sl, tau=0.25)
+    k.view(torch.uint8)[int(t[0, 1]), 1, 3, 100] = 0x7f  # an old key of sequence 0, head 1
+    for tau in (0.25, 0.0):
+        o = mala.mala_decode_paged(q, cache, sl, tau=tau)
+        mala.mala_check()
+        assert torch.isnan(o[0, 2:]).all()
+        assert not torch.isnan(o[0, :2]).any() and not torch.isnan(o[1]).any()
+        if tau:
+            assert torch.equal(o[0, :2], clean[0, :2]) and torch.equal(o[1], clean[1])
+
+
+def test_decode_pages_outside_the_pool_and_lengths_beyond_the_bound():
+    lens = [300, 200, 260, 0]
+    tensors = filled(lens, 2, 32, "plain", 13)
+    t = tensors[4]
+    q = torch.randn((4, 4, 128), device="cuda", generator=gen(6)).to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    good = mala.mala_decode_paged(q, cache, sl, tau=0.0)
+    mala.mala_check()
+    saved = int(t[0, 4])
+    for bad in (-1, tensors[0].shape[0], 2 ** 31 - 1):
+        t[0, 4] = bad
+        for tau in (0.0, 1.0):
+            o = mala.mala_decode_paged(q, cache, sl, tau=tau)
+            with pytest.raises(mala.MalaError, match="MALA_ERR_BAD_PAGE"):
+                mala.mala_check()
+            assert torch.isnan(o[0]).all() and not torch.isnan(o[1:]).any()
+            if tau == 0.0:
+                assert torch.equal(o[1:], good[1:])
+    t[0, 4] = saved
+    o = mala.mala_decode_paged(q, cache, sl, tau=0.0, max_seqlen=256)  # lengths 300 and 260
+    with pytest.raises(mala.MalaError, match="MALA_ERR_BAD_PAGE"):
+        mala.mala_check()
+    assert torch.isnan(o[0]).all() and torch.isnan(o[2]).all()
+    assert not torch.isnan(o[1]).any() and (o[3] == 0).all()
+    sl[1] = 10 ** 9  # far beyond the table
+    o = mala.mala_decode_paged(q, cache, sl, tau=0.0)
+    with pytest.raises(mala.MalaError, match="MALA_ERR_BAD_PAGE"):
+        mala.mala_check()
+    assert torch.isnan(o[1]).all() and torch.equal(o[0], good[0])
+    mala.mala_check()  # reported once
+    sl[1] = -5
+    assert (mala.mala_decode_paged(q, cache, sl, tau=0.0)[1] == 0).all()
+    mala.mala_check()
+
+
+def test_decode_pages_beyond_32_bit_offsets():
+    """A pool of more than 2^32 bytes, its last and first pages in one sequence."""
+    Hkv, page = 8, 128
+    n_pages = (2 ** 32) // (Hkv * page * 128) + 40
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GiB")
+    k = torch.empty((n_pages, Hkv, page, 128), dtype=torch.uint8, device="cuda").view(f8)
+    v = torch.empty((n_pages, Hkv, page, 128), dtype=torch.uint8, device="cuda").view(f8)
+    ks, vs = (torch.ones((n_pages, Hkv), device="cuda") for _ in range(2))
+    t = torch.tensor([[n_pages - 1, 0, n_pages - 2, n_pages // 2 + 3]], dtype=i32, device="cuda")
+    n, H = 4 * page, 2 * Hkv
+    g = gen(17)
+    x = torch.randn((n, 2 * Hkv + H, 128), device="cuda", generator=g).to(bf16)
+    lens = torch.tensor([n], dtype=i32, device="cuda")
+    cache = mala.PagedCache(k, v, ks, vs, t)
+    cu = torch.tensor([0, n], dtype=i32, device="cuda")
+    mala.mala_cache_append(cache, x[:, :Hkv], x[:, Hkv:2 * Hkv], lens, cu_seqlens=cu)
+    K, V = mala.mala_cache_gather(cache, cu, n, n)
+    q = x[-1:, 2 * Hkv:].contiguous()
+    o = mala.mala_decode_paged(q, cache, lens, tau=0.0)
+    mala.mala_check()
+    small = t[0].long()
+    ref = R.RefCache(*(torch.zeros((4, Hkv, page, 128), dtype=torch.uint8),) * 2,
+                     *(torch.ones(4, Hkv),) * 2, torch.arange(4)[None])
+    ref.append(x[:, :Hkv], x[:, Hkv:2 * Hkv], [n], [0, n])
+    ref.check(k.view(torch.uint8)[small], v.view(torch.uint8)[small], ks[small], vs[small])
+    kv = [(ref.val[w] * ref.scale[w][:, :, None, None]).transpose(1, 0, 2, 3).reshape(Hkv, -1, 128)
+          for w in range(2)]
+    assert np.array_equal(as_f64(K), kv[0].transpose(1, 0, 2))
+    assert np.array_equal(as_f64(V), kv[1].transpose(1, 0, 2))
+    r = oracle.decode(as_f64(q)[0], kv[0], kv[1], tau=0.0)
+    for h in range(H):
+        tol = R.decode_bound(as_f64(q)[0, h], kv[0][h // 2], kv[1][h // 2], r["o"][h],
+                             np.ones(n, bool))
+        assert (np.abs(as_f64(o)[0, h] - r["o"][h]) <= tol).all()
+
+
+# ---------------------------------------------------------------------------- append
+def projection(T, Hq, Hkv, g, size=1.0):
+    x = torch.randn((T, Hq + 2 * Hkv, 128), device="cuda", generator=g) * size
+    x *= torch.where(torch.rand((Hq + 2 * Hkv, 128), device="cuda", generator=g) < 0.05, 8.0, 1.0)
+    x = x.to(bf16)
+    return x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+
+
+def check_q(q_out, want, tol):
+    got = as_f64(q_out)
+    rows = ~np.isnan(want)
+    assert (np.abs(got - want)[rows] <= (2.0 ** -8 * np.abs(want) + tol * (1 + 2.0 ** -8))[rows]).all()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("rot,inter", [(128, False), (128, True), (64, False), (96, True), (0, False)])
+def test_append_prompts_chunks_and_steps(page, layout, rot, inter):
+    """Three calls on one cache: prompts of many lengths, chunks behind them, single tokens."""
+    g = gen(page + rot)
+    Hq, Hkv = 6, 2
+    first = [1, 2, page - 1, page, page + 1, 3 * page + 5, 300, 0]
+    chunk = [5, 0, 2, page, 2 * page - 1, 1, 130, 0]
+    final = [a + b + 1 if a + b else 0 for a, b in zip(first, chunk)]
+    n_pages = pages_needed(final, page) + 2
+    k_pages, v_pages, ks, vs = new_pool(n_pages, Hkv, page, layout)
+    t = table_for(final, page, n_pages, g)
+    cache = mala.PagedCache(k_pages, v_pages, ks, vs, t)
+    ref = R.RefCache(k_pages, v_pages, ks, vs, t)
+    freq = (1e4 ** (-torch.arange(rot // 2, device="cuda") / (rot // 2 or 1))).float() if rot else None
+    lens = [0] * 8
+    for step, (news, size) in enumerate(((first, 0.1), (chunk, 1.0), (None, 3.0))):
+        if news is None:  # one token each; the last sequence is an unused slot
+            lens, cu, T = final, None, 8
+        else:
+            lens = [a + b for a, b in zip(lens, news)]
+            cu = np.concatenate([[0], np.cumsum(news)]).tolist()
+            T = cu[-1] + 4  # rows behind the last sequence
+        q, k, v = projection(T, Hq, Hkv, g, size)
+        sl = torch.tensor(lens, dtype=i32, device="cuda")
+        cut = None if cu is None else torch.tensor(cu, dtype=i32, device="cuda")
+        q_out = torch.full((T, Hq, 128), 777.0, dtype=bf16, device="cuda")
+        mala.mala_cache_append(cache, k, v, sl, cu_seqlens=cut, inv_freq=freq, interleaved=inter,
+                               q=q, q_out=q_out, max_new=None if news is None else max(news))
+        mala.mala_check()
+        want, tol = ref.append(k, v, lens, cu, freq, inter, q)
+        ref.check(k_pages, v_pages, ks, vs)
+        check_q(q_out, want, tol)
+        assert (q_out[torch.tensor(np.isnan(want[:, 0, 0]))] == 777.0).all()
+
+
+def test_append_scales_grow_and_hold():
+    """Tokens of growing, shrinking, zero, tiny, huge and non-finite values into one page."""
+    page = 32
+    k_pages, v_pages, ks, vs = new_pool(2, 1, page)
+    t = torch.tensor([[1]], dtype=i32, device="cuda")
+    cache = mala.PagedCache(k_pages, v_pages, ks, vs, t)
+    ref = R.RefCache(k_pages, v_pages, ks, vs, t)
+    g = gen(3)
+    sizes = [0.0, 1e-38, 1e-3, 1.0, 1e3, 1e-2, 1e37, 1.0, 448.0, 0.0]
+    for i, size in enumerate(sizes):
+        x = (torch.randn((2, 1, 1, 128), device="cuda", generator=g).clamp(-2, 2) * size).to(bf16)
+        if i == 5:
+            x[0, 0, 0, 3], x[0, 0, 0, 4], x[1, 0, 0, 5] = float("inf"), float("nan"), -float("inf")
+        if i == 8:
+            x[:] = 448.0  # the largest value of its scale exactly
+        n = torch.tensor([i + 1], dtype=i32, device="cuda")
+        mala.mala_cache_append(cache, x[0], x[1], n)
+        mala.mala_check()
+        ref.append(x[0], x[1], [i + 1])
+        ref.check(k_pages, v_pages, ks, vs)
+
+
+def test_append_far_positions():
+    """Angles of positions where float32 products have lost them."""
+    page, n = 128, 500_000
+    width = -(-n // page)
+    k_pages, v_pages, ks, vs = new_pool(3, 2, page)
+    t = torch.full((1, width), 99, dtype=i32, device="cuda")
+    t[0, -3:] = torch.tensor([2, 0, 1], dtype=i32)
+    cache = mala.PagedCache(k_pages, v_pages, ks, vs, t)
+    ref = R.RefCache(k_pages, v_pages, ks, vs, t)
+    m = (n - 1) % page + 1 + 150
+    q, k, v = projection(m, 4, 2, gen(9))
+    freq = (5e5 ** (-torch.arange(64, device="cuda") / 64)).float()
+    lens, cu = [n], [0, m]
+    q_out = mala.mala_cache_append(cache, k, v, torch.tensor(lens, dtype=i32, device="cuda"),
+                                   cu_seqlens=torch.tensor(cu, dtype=i32, device="cuda"),
+                                   inv_freq=freq, q=q)
+    mala.mala_check()
+    want, tol = ref.append(k, v, lens, cu, freq, False, q)
+    check_q(q_out, want, tol)
+    # the first page's rows before the new tokens were NaN bytes with a NaN scale:
+    # they stay NaN, and the page's scale is the new tokens'
+    ref.check(k_pages, v_pages, ks, vs)
+
+
+def test_append_in_place_queries_and_one_row_views():
+    g = gen(21)
+    k_pages, v_pages, ks, vs = new_pool(4, 1, 16)
+    t = torch.tensor([[0, 1], [2, 3]], dtype=i32, device="cuda")
+    cache = mala.PagedCache(k_pages, v_pages, ks, vs, t)
+    q, k, v = projection(2, 3, 1, g)
+    freq = torch.rand(64, device="cuda", generator=g)
+    sl = torch.tensor([17, 4], dtype=i32, device="cuda")
+    ref = R.RefCache(k_pages, v_pages, ks, vs, t)
+    want, tol = ref.append(k, v, [17, 4], None, freq, False, q)
+    other = mala.mala_cache_append(cache, k, v, sl, inv_freq=freq, q=q)
+    same = mala.mala_cache_append(cache, k, v, sl, inv_freq=freq, q=q, q_out=q)
+    mala.mala_check()
+    assert same is q and torch.equal(other, q)
+    check_q(q, want, tol)
+    # a page table's second page of sequence 0: rows before position 17 were never written
+    assert int(ks.isnan().sum()) == 2
+
+
+def test_append_what_does_not_fit_is_left_out():
+    g = gen(22)
+    page = 16
+    k_pages, v_pages, ks, vs = new_pool(6, 2, page)
+    t = torch.tensor([[0, 1], [2, 55], [3, 4], [5, 5]], dtype=i32, device="cuda")
+    cache = mala.PagedCache(k_pages, v_pages, ks, vs, t)
+    q, k, v = projection(60, 2, 2, g)
+
+    def call(lens, cu, max_new=60):
+        ref = R.RefCache(k_pages, v_pages, ks, vs, t)
+        mala.mala_cache_append(cache, k, v, torch.tensor(lens, dtype=i32, device="cuda"),
+                               cu_seqlens=torch.tensor(cu, dtype=i32, device="cuda"),
+                               max_new=max_new)
+        ok = True
+        try:
+            mala.mala_check()
+        except mala.MalaError as e:
+            assert e.code == 6
+            ok = False
+        return ref, ok
+
+    ref, ok = call([20, 20, 20, 0], [0, 20, 40, 60, 60])  # sequence 1's second page is no page
+    ref.append(k, v, [20, 20, 20, 0], [0, 20, 40, 60, 60])
+    assert not ok
+    ref.check(k_pages, v_pages, ks, vs)
+    ref, ok = call([20, 3, 20, 0], [0, 5, 10, 12, 12])  # sequence 1 has more new tokens than length
+    ref.append(k, v, [20, 3, 20, 0], [0, 5, 10, 12, 12])
+    assert not ok
+    ref.check(k_pages, v_pages, ks, vs)
+    ref, ok = call([20, 16, 32, 0], [0, 5, 10, 26, 26], max_new=8)  # sequence 2: 16 > 8
+    ref.append(k, v, [20, 16, 32, 0], [0, 5, 10, 26, 26], max_new=8)
+    assert not ok
+    ref.check(k_pages, v_pages, ks, vs)
+    for cu in ([-3, 0, 0, 0, 0], [0, 0, 0, 100, 100], [0, 61, 61, 61, 61]):  # rows that are not there
+        ref, ok = call([20, 16, 32, 0], cu)
+        assert not ok
+        ref.check(k_pages, v_pages, ks, vs)
+    ref, ok = call([33, 0, 0, 0], [0, 5, 5, 5, 5])  # past the table: position 32
+    ref.append(k, v, [33, 0, 0, 0], [0, 5, 5, 5, 5])
+    assert not ok
+    ref.check(k_pages, v_pages, ks, vs)
+    ref, ok = call([0, -4, 0, 0], [0, 5, 9, 9, 9])  # unused slots: nothing, and nothing to report
+    assert ok
+    ref.check(k_pages, v_pages, ks, vs)
+
+
+# ---------------------------------------------------------------------------- gather
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_gather(page, layout):
+    lens = [1, 0, page, page - 1, page + 1, 700, 129]
+    Hkv = 3
+    tensors = filled(lens, Hkv, page, layout, 300 + page)
+    cache = mala.PagedCache(*tensors)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    total = int(cu[-1]) + 5
+    out = tuple(torch.full((total, Hkv, 128), 55.0, dtype=bf16, device="cuda") for _ in range(2))
+    K, V = mala.mala_cache_gather(cache, torch.tensor(cu, dtype=i32, device="cuda"), max(lens),
+                                  total, out=out)
+    mala.mala_check()
+    assert K is out[0] and V is out[1]
+    for b, n in enumerate(lens):
+        if n:
+            for got, want in zip((K, V), R.sequence(tensors[:4], tensors[4], b, n)):
+                assert np.array_equal(as_f64(got[cu[b]:cu[b + 1]]), want.transpose(1, 0, 2))
+    assert (K[cu[-1]:] == 55.0).all() and (V[cu[-1]:] == 55.0).all()
+
+
+def test_gather_refusals_on_the_device():
+    lens = [40, 20, 50]
+    tensors = filled(lens, 2, 16, "plain", 31)
+    t = tensors[4]
+    cache = mala.PagedCache(*tensors)
+    total = 110
+
+    def call(cu, max_seqlen):
+        out = tuple(torch.full((total, 2, 128), 55.0, dtype=bf16, device="cuda") for _ in range(2))
+        mala.mala_cache_gather(cache, torch.tensor(cu, dtype=i32, device="cuda"), max_seqlen, total,
+                               out=out)
+        with pytest.raises(mala.MalaError, match="MALA_ERR_BAD_PAGE"):
+            mala.mala_check()
+        return out
+
+    K, V = call([0, 40, 60, 110], 45)  # the third is longer than the bound
+    assert (K[60:] == 55.0).all() and not (K[:60] == 55.0).all(-1).any()
+    K, V = call([0, 40, 60, 120], 60)  # rows past the end
+    assert (V[60:] == 55.0).all()
+    t[1, 1] = -1
+    K, V = call([0, 40, 60, 110], 50)
+    assert torch.isnan(K[56:60]).all() and torch.isnan(V[56:60]).all()
+    assert not torch.isnan(K[:56]).any() and not torch.isnan(K[60:]).any()
+
+
+# ---------------------------------------------------------------------------- together
+def test_serving_run_matches_the_prefill_and_decode_over_a_whole_cache():
+    """Prompts in two chunks (append, gather, mala_fwd_varlen), then steps (append, decode):
+    decode's keep sets and outputs against mala_decode over the same values as a contiguous
+    bf16 cache, the prefill's last row against a decode of the same query."""
+    g = gen(41)
+    Hq, Hkv, page = 8, 2, 32
+    prompts = [300, 45, 1000]
+    B, steps = 3, 4
+    final = [n + steps for n in prompts]
+    n_pages = pages_needed(final, page)
+    k_pages, v_pages, ks, vs = new_pool(n_pages, Hkv, page)
+    t = table_for(final, page, n_pages, g)
+    cache = mala.PagedCache(k_pages, v_pages, ks, vs, t)
+    freq = (1e4 ** (-torch.arange(64, device="cuda") / 64)).float()
+    done = [0] * B
+    for part in (0.6, 1.0):
+        news = [round(part * n) - d for n, d in zip(prompts, done)]
+        done = [d + m for d, m in zip(done, news)]
+        cu = torch.tensor([0, *np.cumsum(news)], dtype=i32, device="cuda")
+        cu_k = torch.tensor([0, *np.cumsum(done)], dtype=i32, device="cuda")
+        lens = torch.tensor(done, dtype=i32, device="cuda")
+        q, k, v = projection(sum(news), Hq, Hkv, g)
+        q = mala.mala_cache_append(cache, k, v, lens, cu_seqlens=cu, max_new=max(news),
+                                   inv_freq=freq, q=q)
+        K, V = mala.mala_cache_gather(cache, cu_k, max(done), sum(done))
+        O, LSE = mala.mala_fwd_varlen(q, K, V, cu, cu_k, max(news), max(done), tau=0.0)
+        last = (cu[1:] - 1).long()
+        o = mala.mala_decode_paged(q[last].contiguous(), cache, lens, tau=0.0)
+        mala.mala_check()
+        assert rel_l2(as_f64(O[last]), as_f64(o)) <= 4e-3  # both within 2e-3 of the formula
+    for _ in range(steps):
+        done = [d + 1 for d in done]
+        lens += 1
+        q, k, v = projection(B, Hq, Hkv, g)
+        q = mala.mala_cache_append(cache, k, v, lens, inv_freq=freq, q=q)
+        for tau in (1.0, 0.0):
+            o, kept, bits = mala.mala_decode_paged(q, cache, lens, tau=tau, trace=True)
+            mala.mala_check()
+            for b, n in enumerate(done):
+                K, V = (torch.tensor(x).to(bf16).cuda()[None].contiguous()
+                        for x in R.sequence((k_pages, v_pages, ks, vs), t, b, n))
+                o2, kept2, bits2 = mala.mala_decode(q[b:b + 1].contiguous(), K, V, tau=tau, trace=True)
+                mala.mala_check()
+                assert torch.equal(kept2[0], kept[b])
+                assert torch.equal(bits2[0], bits[b, :, :bits2.shape[2]])
+                assert rel_l2(as_f64(o[b]), as_f64(o2[0])) <= 4e-3
+
+
+def test_steps_in_a_graph_and_on_two_streams():
+    """A captured step (lengths + 1, append, decode) replayed against eager calls; two captured
+    graphs of two caches replayed at once on two streams."""
+    def setup(seed):
+        g = gen(seed)
+        Hq, Hkv, page, lens = 8, 2, 16, [30, 1, 500, 0]
+        room = [n + 20 for n in lens]
+        n_pages = pages_needed(room, page)
+        k, v, ks, vs = new_pool(n_pages, Hkv, page)
+        t = table_for(room, page, n_pages, g, spare=0)
+        cache = mala.PagedCache(k, v, ks, vs, t)
+        T = sum(lens)
+        _, kk, vv = projection(T, Hq, Hkv, g)
+        sl = torch.tensor(lens, dtype=i32, device="cuda")
+        freq = torch.rand(64, device="cuda", generator=g)
+        mala.mala_cache_append(cache, kk, vv, sl, cu_seqlens=torch.tensor(
+            [0, *np.cumsum(lens)], dtype=i32, device="cuda"), inv_freq=freq)
+        x = torch.randn((4, Hq + 2 * Hkv, 128), device="cuda", generator=g).to(bf16)
+        used = (sl > 0).int()
+
+        def step():
+            sl.add_(used)  # the unused slot stays at 0
+            q = mala.mala_cache_append(cache, x[:, 8:10], x[:, 10:], sl, inv_freq=freq, q=x[:, :8])
+            return mala.mala_decode_paged(q, cache, sl, tau=1.0)
+        return step, x, g, (k, v, ks, vs, sl)
+
+    eager, xe, ge, se = setup(51)
+    steps, graphs, outs, states, inputs = [], [], [], [], []
+    for _ in range(2):
+        step, x, g, st = setup(51)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            o = step()
+        graphs.append((graph, s))
+        steps.append(step)  # keeps the cache and its page table, which the graph reads
+        outs.append(o)
+        states.append(st)
+        inputs.append(x)
+    torch.cuda.synchronize()
+    for _ in range(12):
+        fresh = torch.randn(xe.shape, device="cuda", generator=ge).to(bf16)
+        want = None
+        xe.copy_(fresh)
+        want = eager()
+        for x in inputs:
+            x.copy_(fresh)
+        torch.cuda.synchronize()
+        for graph, s in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for o, st in zip(outs, states):
+            assert torch.equal(o, want)
+            for a, b in zip(st, se):
+                if a.dtype == f8:
+                    a, b = a.view(torch.uint8), b.view(torch.uint8)
+                assert torch.equal(a.nan_to_num(7.0) if a.is_floating_point() else a,
+                                   b.nan_to_num(7.0) if b.is_floating_point() else b)
+    mala.mala_check()
+
+
+def test_a_page_shared_by_two_sequences_is_read_by_both():
+    lens = [96, 90]
+    tensors = list(filled([96], 2, 32, "plain", 61))
+    t = tensors[4]
+    tensors[4] = torch.stack([t[0], t[0]])[:, :3].contiguous()
+    q = torch.randn((1, 4, 128), device="cuda", generator=gen(8)).to(bf16).repeat(2, 1, 1)
+    cache = mala.PagedCache(*tensors)
+    o = mala.mala_decode_paged(q, cache, torch.tensor(lens, dtype=i32, device="cuda"), tau=0.0)
+    mala.mala_check()
+    assert check_decode(tensors, lens, q, o, 0.0, False) == 8
