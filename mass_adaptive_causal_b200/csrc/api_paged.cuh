@@ -48,9 +48,37 @@ inline mala_status make_pool(const mala_paged_cache* c, paged::Pool* p) {
   p->table_stride = c->table_stride;
   p->num_pages = c->num_pages;
   p->page = c->page_size;
+  p->page_log2 = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
   p->max_pages = c->max_pages;
   p->Hkv = c->Hkv;
   return MALA_OK;
+}
+
+// One side of the pool as a 4-D byte tensor (x = d, y = token, z = head, w =
+// page), a box of min(page, 32) tokens, 128-byte swizzle.
+inline bool make_page_map(CUtensorMap* m, const void* base, const paged::Pool& p, long long page,
+                          long long head, long long tok) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)paged::D, (cuuint64_t)p.page, (cuuint64_t)p.Hkv,
+                        (cuuint64_t)p.num_pages};
+  // the stride of a dimension of extent 1 is never used, but has to be legal
+  cuuint64_t strides[3] = {(cuuint64_t)tok, (cuuint64_t)(p.Hkv > 1 ? head : paged::D),
+                           (cuuint64_t)(p.num_pages > 1 ? page : paged::D)};
+  cuuint32_t box[4] = {(cuuint32_t)paged::D, (cuuint32_t)(p.page < 32 ? p.page : 32), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
+                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Blocks of a decode cluster: a power of two, as many as fill `slots` resident
+// blocks with the call's groups, but no more than leave every warp a piece of work.
+inline int decode_cluster(long long groups, long long pieces, int slots) {
+  int C = 1;
+  while (C < pdec::MAXC && groups * C < slots && (long long)pdec::NW * 2 * C <= pieces) C *= 2;
+  return C;
 }
 
 // An input or output of append: [total][heads][128] bf16 by its strides.
@@ -154,11 +182,43 @@ mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q, void
   p.per_head = per_head;
   p.kept_tiles = kept_tiles;
   p.keep_bits = keep_bits;
-  const size_t smem = mala::pdec::smem_bytes(p.G, p.max_tiles);
-  if (smem > 220 * 1024) return MALA_ERR_TOO_LARGE;
-  MALA_CUDA_TRY(cudaFuncSetAttribute(mala::pdec::decode_kernel,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  mala::pdec::decode_kernel<<<dim3(Hkv, batch), mala::pdec::NT, smem, as_stream(stream)>>>(p);
+  CUtensorMap mk, mv;
+  if (!make_page_map(&mk, p.pool.k, p.pool, p.pool.k_page, p.pool.k_head, p.pool.k_tok) ||
+      !make_page_map(&mv, p.pool.v, p.pool, p.pool.v_page, p.pool.v_head, p.pool.v_tok))
+    return MALA_ERR_CUDA;
+  // a single tile is always kept: exact attention is the rule's answer
+  const bool dense = tau == 0.f || p.max_tiles == 1;
+  const long long groups = (long long)batch * Hkv;
+  const int nsm = sm_count();
+  size_t smem = mala::pdec::DENSE_SMEM;
+  if (dense) {
+    p.C = decode_cluster(groups, ((long long)p.max_tiles * 128) / mala::pdec::CK, nsm);
+  } else {
+    p.C = decode_cluster(groups, p.max_tiles, 2 * nsm);
+    // the statistics of the longest sequence have to fit beside the ring
+    while (p.C < mala::pdec::MAXC && mala::pdec::rule_smem(p.G, p.max_tiles, p.C) > 112 * 1024)
+      p.C *= 2;
+    smem = mala::pdec::rule_smem(p.G, p.max_tiles, p.C);
+    if (smem > 220 * 1024) return MALA_ERR_TOO_LARGE;
+  }
+  for (int c = p.C; c > 1; c >>= 1) ++p.C_log2;
+  auto kernel = dense ? mala::pdec::dense_kernel : mala::pdec::rule_kernel;
+  MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  if (p.C > 8)
+    MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.C, Hkv, batch);
+  cfg.blockDim = dim3(mala::pdec::NT, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = as_stream(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MALA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, mk, mv, p));
   return launch_status();
 }
 

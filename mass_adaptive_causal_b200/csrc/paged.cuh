@@ -31,7 +31,7 @@ struct Pool {
   const int32_t* table;  // [sequences][max_pages], rows table_stride apart
   long long k_page, k_head, k_tok, v_page, v_head, v_tok;  // strides in bytes
   long long table_stride;
-  int num_pages, page, max_pages, Hkv;
+  int num_pages, page, page_log2, max_pages, Hkv;
 };
 
 // The page that holds position `pos` of sequence b, or -1 (and a status) when
