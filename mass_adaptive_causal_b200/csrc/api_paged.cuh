@@ -2,6 +2,8 @@
 // checks and launches (the contract is in include/mala.h).
 #pragma once
 
+#include <atomic>
+
 #include "api.cuh"
 #include "decode_paged_sm100.cuh"
 #include "paged.cuh"
@@ -55,7 +57,7 @@ inline mala_status make_pool(const mala_paged_cache* c, paged::Pool* p) {
 }
 
 // One side of the pool as a 4-D byte tensor (x = d, y = token, z = head, w =
-// page), a box of min(page, 32) tokens, 128-byte swizzle.
+// page), a box of one page and head, 128-byte swizzle.
 inline bool make_page_map(CUtensorMap* m, const void* base, const paged::Pool& p, long long page,
                           long long head, long long tok) {
   auto enc = encode_fn();
@@ -65,7 +67,7 @@ inline bool make_page_map(CUtensorMap* m, const void* base, const paged::Pool& p
   // the stride of a dimension of extent 1 is never used, but has to be legal
   cuuint64_t strides[3] = {(cuuint64_t)tok, (cuuint64_t)(p.Hkv > 1 ? head : paged::D),
                            (cuuint64_t)(p.num_pages > 1 ? page : paged::D)};
-  cuuint32_t box[4] = {(cuuint32_t)paged::D, (cuuint32_t)(p.page < 32 ? p.page : 32), 1, 1};
+  cuuint32_t box[4] = {(cuuint32_t)paged::D, (cuuint32_t)p.page, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -73,12 +75,52 @@ inline bool make_page_map(CUtensorMap* m, const void* base, const paged::Pool& p
   return r == CUDA_SUCCESS;
 }
 
-// Blocks of a decode cluster: a power of two, as many as fill `slots` resident
-// blocks with the call's groups, but no more than leave every warp a piece of work.
-inline int decode_cluster(long long groups, long long pieces, int slots) {
-  int C = 1;
-  while (C < pdec::MAXC && groups * C < slots && (long long)pdec::NW * 2 * C <= pieces) C *= 2;
-  return C;
+// Clusters of C blocks of a decode kernel that the device holds at once, with one or two
+// blocks to an SM. What the driver says is kept: the question takes microseconds.
+inline int resident_clusters(bool wide, bool rule, int C, size_t smem) {
+  static std::atomic<int> known[2][2][2][pdec::MAXC + 1];  // 0: not asked yet
+  std::atomic<int>& k = known[wide][rule][smem <= 113 * 1024][C];
+  int n = k.load(std::memory_order_relaxed);
+  if (n > 0) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C, 1, 1);
+  cfg.blockDim = dim3(pdec::NT, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, pdec::decode_kernel_of(wide ? pdec::GMAX : 1, rule),
+                                     &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  k.store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// Blocks of a decode cluster, 0 when the statistics of the longest sequence do not fit.
+inline int decode_cluster(const pdec::Params& p, long long groups, bool rule, size_t* smem) {
+  int best = 0;
+  double least = 0;
+  for (int C = 1; C <= pdec::MAXC; ++C) {
+    if (best > 0 && C > p.max_tiles) break;
+    const size_t need = pdec::smem_bytes(p.G, p.max_tiles, C, p.per_head, rule);
+    if (need > pdec::MAX_SMEM) continue;
+    const int resident = resident_clusters(p.G > 4, rule, C, need);
+    if (resident < 1) continue;
+    const double waves = (double)((groups + resident - 1) / resident);
+    const double cost = waves * ((double)((p.max_tiles + C - 1) / C) + 8.0);
+    if (best == 0 || cost < least) {
+      best = C;
+      least = cost;
+      *smem = need;
+    }
+  }
+  return best;
 }
 
 // An input or output of append: [total][heads][128] bf16 by its strides.
@@ -168,16 +210,16 @@ mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q, void
     if (reinterpret_cast<uintptr_t>(w) & 3u) return MALA_ERR_INVALID_ARG;
   const int held = cache->max_pages * cache->page_size;
   if (max_seqlen <= 0) max_seqlen = held;
-  const int nt = (int)(((long long)max_seqlen + 127) / 128);
+  p.nw = (int)(((long long)max_seqlen + 4095) / 4096);  // trace rows: the caller's max_seqlen
+  p.max_len = max_seqlen < held ? max_seqlen : held;
+  p.max_tiles = (p.max_len + 127) / 128;
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.o = reinterpret_cast<__nv_bfloat16*>(o);
   p.seq_lens = seq_lens;
   p.G = Hq / Hkv;
+  p.GP = (p.G + 1) & ~1;
   p.Hkv = Hkv;
-  p.nw = (nt + 31) / 32;  // trace rows are laid out by the caller's max_seqlen
-  p.max_tiles = nt < (held + 127) / 128 ? nt : (held + 127) / 128;
   p.scale_log2 = resolve_scale(scale, mala::paged::D) * mala::kLog2e;
-  p.never_skip = tau == 0.f;
   p.log2_tau = tau > 0.f ? log2f(tau) : 0.f;
   p.per_head = per_head;
   p.kept_tiles = kept_tiles;
@@ -187,25 +229,14 @@ mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q, void
       !make_page_map(&mv, p.pool.v, p.pool, p.pool.v_page, p.pool.v_head, p.pool.v_tok))
     return MALA_ERR_CUDA;
   // a single tile is always kept: exact attention is the rule's answer
-  const bool dense = tau == 0.f || p.max_tiles == 1;
-  const long long groups = (long long)batch * Hkv;
-  const int nsm = sm_count();
-  size_t smem = mala::pdec::DENSE_SMEM;
-  if (dense) {
-    p.C = decode_cluster(groups, ((long long)p.max_tiles * 128) / mala::pdec::CK, nsm);
-  } else {
-    p.C = decode_cluster(groups, p.max_tiles, 2 * nsm);
-    // the statistics of the longest sequence have to fit beside the ring
-    while (p.C < mala::pdec::MAXC && mala::pdec::rule_smem(p.G, p.max_tiles, p.C) > 112 * 1024)
-      p.C *= 2;
-    smem = mala::pdec::rule_smem(p.G, p.max_tiles, p.C);
-    if (smem > 220 * 1024) return MALA_ERR_TOO_LARGE;
-  }
-  for (int c = p.C; c > 1; c >>= 1) ++p.C_log2;
-  auto kernel = dense ? mala::pdec::dense_kernel : mala::pdec::rule_kernel;
-  MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  if (p.C > 8)
-    MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  const bool rule = tau > 0.f && p.max_tiles > 1;
+  const mala::pdec::Kernel kernel = mala::pdec::decode_kernel_of(p.G, rule);
+  MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)mala::pdec::MAX_SMEM));
+  MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  size_t smem;
+  p.C = decode_cluster(p, (long long)batch * Hkv, rule, &smem);
+  if (p.C < 1) return MALA_ERR_TOO_LARGE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.C, Hkv, batch);
   cfg.blockDim = dim3(mala::pdec::NT, 1, 1);

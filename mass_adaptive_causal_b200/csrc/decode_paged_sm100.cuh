@@ -4,29 +4,33 @@
 // every head of the group (or the head alone) has  mt - m - ln l < ln tau -
 // ln Lc.
 //
-// One cluster of C blocks (1 to 16) of eight warps per (sequence, key/value
-// head), one launch, no workspace. A warp owns a ring of 4 KB stages (32 keys
-// or values) that its lane 0 refills by TMA, so that nothing but the warp itself
-// stands between a stage's use and its next load.
+// One cluster of C blocks (1 to 16) per (sequence, key/value head), one launch, no
+// workspace; tile t of the sequence is block t mod C's. A block has four warps that do the
+// softmax (a thread per key of a tile, later per dimension of the output), one that looks
+// pages up and loads tiles by TMA into a ring, and one that issues the matrix products.
 //
-// tau > 0 (rule_kernel):
-//  A  tile t goes to warp t mod 8 C: scores S[key][head] = q . k by mma
-//     m16n8k16 in f16, the tile's row max m_t and mass l_t per head into the
-//     block's shared memory. This reads all of K once, the HBM-bound part;
+// tau > 0 (RULE):
+//  A  scores of every tile, its max m_t and mass l_t per head into the block's shared
+//     memory. This reads all of K once, the HBM-bound part;
 //  B  every block collects the statistics of the whole cluster and replays the
 //     rule over them, newest first: all arrive at the same kept tiles, and the
 //     n-th kept one falls to block n mod C;
-//  C  a warp per quarter of a kept tile: P = exp(S - m) with the final m,
-//     O += P V by mma; the warps' sums are joined in shared memory, the
-//     blocks' through the cluster.
-// tau = 0 (dense_kernel): K and V are read once, side by side; every warp keeps
-// a running max, mass and output, joined at the end.
+//  C  for its kept tiles: P = exp(S - m), O += P V; the blocks' sums are joined through the
+//     cluster.
+// tau = 0: K and V are read once, side by side, with a running max, mass and output.
 //
-// The number formats: e4m3 is exact in f16; q is scaled by a power of two per
-// head so that its largest value is in [2^14, 2^15), where all values within
-// 2^-29 of the largest are exact in f16 and smaller ones are off by at most 2^-39
-// of it, less than a float32 sum's rounding; P is carried as 2^14 p, which keeps
-// eleven bits down to p = 2^-28. Sums are float32.
+// Both products run on tcgen05 in e4m3, straight on the bytes as they lie in the cache:
+// S[key][.] = K q^T with the K tile as the 128-row operand, O[dim][.] = V^T P with the
+// V tile as the (transposed) 128-row operand. (mma.sync has no e4m3 form of its own here: it
+// is widened to f16, which made a warp's integer work the bound at 45% of the copy
+// bandwidth.) The other operand is split into four e4m3 terms, 2^4 apart, in columns of
+// their own, and the columns' sums are joined in float32:
+//  - q, scaled by a power of two per head to have its largest value in [2^7, 2^8): a bf16
+//    value has eight bits, a term carries four, so values within 2^-21 of the largest are
+//    exact, and the rest is off by at most 2^-29 of it;
+//  - P, scaled to 2^8 at the row's reference (its running or final max), is rounded to
+//    f16 and split: exact but for an error of at most 2^-30.
+// Sums are float32; a row's max and mass never leave float32.
 #pragma once
 
 #include "paged.cuh"
@@ -38,788 +42,928 @@ namespace pdec {
 using paged::D;
 using paged::Pool;
 using sm100::ex2_approx;
+using sm100::mbar_arrive;
+using sm100::mbar_expect_tx;
+using sm100::mbar_wait;
+using sm100::smem_u32;
 
 constexpr int T = 128;
 constexpr int GMAX = 8;
-constexpr int NW = 8;
-constexpr int NT = NW * 32;
-constexpr float kPShift = 14.f;      // P is carried as 2^14 p
-constexpr int CK = 32;               // keys of a chunk (one ring stage)
-constexpr uint32_t STAGE = CK * D;   // bytes
-constexpr int MAXC = 16;             // blocks of a cluster
-constexpr int RULE_NST = 3;          // ring stages of a warp
-constexpr int DENSE_NST = 3;         // pairs of stages (K, V) of a warp
-constexpr uint32_t RULE_RING = NW * RULE_NST * STAGE;
-constexpr uint32_t DENSE_RING = NW * DENSE_NST * 2 * STAGE;
+constexpr int NT = 256;               // warps 0 - 3 softmax, 4 loads, 5 products, 6 holds the tensor
+                                      // memory, 6 and 7 help in B
+constexpr int NC = 128;               // softmax threads
+constexpr int W_LOAD = 4, W_MMA = 5, W_TMEM = 6;
+constexpr uint32_t TILE_BYTES = T * D;
+constexpr int NST = 5;                // ring stages (tiles)
+constexpr uint32_t RING = NST * TILE_BYTES;
+constexpr int MAXC = 16;              // blocks of a cluster
+constexpr int NMETA = 16;             // tiles whose scales are held
+constexpr int TERMS = 4;
 
 struct Params {
   Pool pool;
-  const __nv_bfloat16* q;   // [batch][Hq][128]
+  const __nv_bfloat16* q;  // [batch][Hq][128]
   __nv_bfloat16* o;
   const int32_t* seq_lens;
-  int G, Hkv, max_tiles;
-  int C, C_log2;
+  int G, GP, Hkv, max_len, max_tiles, C;  // GP: G rounded up to even
   float scale_log2, log2_tau;
-  int never_skip, per_head;
+  int per_head;
   int32_t* kept_tiles;
   uint32_t* keep_bits;
   int nw;  // words of a keep_bits row
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// ------------------------------------------------------------------ instructions
+// Instruction descriptor of tcgen05.mma kind::f8f6f4, e4m3 operands, float32 sums.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Descriptor of an operand without swizzle whose rows of sixteen bytes run along M or N: `lbo`
+// bytes to the next eight of K, `sbo` to the next sixteen of N.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46;
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+  static_assert(N == 16 || N == 32, "");
+  if constexpr (N == 32) {
+    sm100::tmem_ld32(taddr, v);
+  } else {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
+  }
+}
+// The largest of a warp's values, in every lane; a NaN is passed over.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Whether any softmax thread's predicate holds (a barrier of theirs).
+__device__ __forceinline__ bool any_of_softmax(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sync_softmax() {
+  asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 h) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&h)));
+  return r;
+}
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t x) {
+  const uint32_t h = paged::e4m3x2_to_f16x2(x);
+  return *reinterpret_cast<const __half2*>(&h);
 }
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The cluster's barrier, for threads that need not be together with their warp's others.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 
-// B fragments of the group's heads for S = K q^T. The order of a sum's terms
-// is free, so thread c = lane % 4 takes dimensions 32 c .. 32 c + 31 (the bytes
-// it loads of a key) instead of the fragment's own columns: k-step ks covers
-// dimensions 32 c + 4 ks .. + 3. Returns the factor that undoes head n =
-// lane / 4's scaling.
-__device__ __forceinline__ float load_q(const __nv_bfloat16* q, int G, uint32_t (&bq)[8][2]) {
-  const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
-  float x[32];
+// ------------------------------------------------------------------ shared memory
+// What the softmax threads need to know of a tile: its first position, the heads
+// that keep it, and the scales of each sixteen tokens (0 where there are none).
+struct alignas(16) Meta {
+  int pos;
+  uint32_t heads;
+  int pad[2];
+  float k[8], v[8];
+};
+
+template <int GH>
+struct Shared {
+  unsigned char p[2][T * TERMS * GH];  // P of a tile: key k's terms in rows of sixteen bytes
+  unsigned char q[TERMS * GH * D];     // q's terms [term][head][128], 128-byte swizzle
+  Meta meta[NMETA];
+  float2 part[2][4][GH];               // a tile's statistics by warp
+  uint64_t full[NST], empty[NST];
+  uint64_t s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2];
+  float undo[GMAX];                    // what a head's products are multiplied with
+  float mfin[GMAX], lfin[GMAX];        // final max (log2 units) and mass
+  float wm[4][GMAX];
+  int bad, abort, items;
+  uint32_t tmem;
+};
+
+// The end of the kernel, in the ring's space: what the cluster's blocks send each other.
+struct Join {
+  float recv[GMAX * (D + MAXC)];  // partial outputs of this block's dimensions, by sender
+  float2 ml[MAXC][GMAX];
+  int bad[MAXC];
+};
+
+// Shared memory behind the ring and Shared: statistics [slots][GP] of tiles t = slot C + rank, the
+// keep bits [units][words], this block's items.
+__host__ __device__ inline int rule_slots(int max_tiles, int C) { return (max_tiles + C - 1) / C; }
+__host__ __device__ inline int rule_words(int max_tiles) { return (max_tiles + 31) / 32; }
+inline size_t smem_bytes(int G, int max_tiles, int C, bool per_head, bool rule) {
+  const int GP = (G + 1) & ~1;
+  size_t n = RING + (G > 4 ? sizeof(Shared<8>) : sizeof(Shared<4>));
+  if (rule)
+    n += (size_t)rule_slots(max_tiles, C) * (GP * sizeof(float2) + sizeof(uint32_t)) +
+         (size_t)rule_words(max_tiles) * (per_head ? G : 1) * sizeof(uint32_t);
+  return n;
+}
+constexpr size_t MAX_SMEM = 224 * 1024;
+
+// ------------------------------------------------------------------ pieces of the kernel
+// q's terms into shared memory: sixteen threads a head, eight dimensions each. `raw` was
+// loaded by thread tid for head tid / 16 (zero for a head that is not there).
+template <int GH>
+__device__ __forceinline__ void split_q(const uint4& raw, Shared<GH>& sh, float scale_log2) {
+  const int tid = threadIdx.x, g = tid >> 4, c = tid & 15;
+  float x[8];
+  paged::unpack8(raw, x);
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (n < G) u = *reinterpret_cast<const uint4*>(q + n * D + 32 * c + 8 * i);
-    float y[8];
-    paged::unpack8(u, y);
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[8 * i + e] = y[e];
-      amax = fmaxf(amax, fabsf(y[e]));
-    }
-  }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  for (int d = 1; d < 16; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  if (g >= GH) return;
   int e = (int)(__float_as_uint(amax) >> 23);  // biased exponent
-  e = e < 30 ? 30 : (e > 240 ? 240 : e);
-  const float up = __uint_as_float((uint32_t)(127 + 14 - (e - 127)) << 23);
+  e = e < 8 ? 8 : (e > 254 ? 254 : e);
+  const float up = __uint_as_float((uint32_t)(261 - e) << 23);
+  if (c == 0) sh.undo[g] = __uint_as_float((uint32_t)(e - 7) << 23) * scale_log2;
 #pragma unroll
-  for (int ks = 0; ks < 8; ++ks) {
-    bq[ks][0] = pack_f16(x[4 * ks] * up, x[4 * ks + 1] * up);
-    bq[ks][1] = pack_f16(x[4 * ks + 2] * up, x[4 * ks + 3] * up);
+  for (int i = 0; i < 8; ++i) {
+    x[i] *= up;
+    if (!(fabsf(x[i]) < 512.f)) x[i] = __int_as_float(0x7fc00000);  // infinity: e4m3 has none
   }
-  return __uint_as_float((uint32_t)(127 - 14 + (e - 127)) << 23);
-}
-
-using sm100::mbar_expect_tx;
-using sm100::mbar_wait;
-using sm100::smem_u32;
-
-// Scores (raw, of the scaled q) of the sixteen keys whose rows lie at `blk` in
-// the 128-byte swizzle: row r's 16-byte chunk i is at r * 128 + ((i ^ r % 8) * 16).
-// Thread (r, c) takes keys r and r + 8, chunks 2 c and 2 c + 1: the eight lanes of
-// a quarter-warp touch all eight chunk positions.
-__device__ __forceinline__ void scores16(const unsigned char* blk, const uint32_t (&bq)[8][2],
-                                         float (&acc)[4]) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const uint32_t o0 = r * 128 + (((2 * c) ^ r) << 4), o1 = r * 128 + (((2 * c + 1) ^ r) << 4);
-  uint4 a[2], b[2];
-  a[0] = *reinterpret_cast<const uint4*>(blk + o0);
-  a[1] = *reinterpret_cast<const uint4*>(blk + o1);
-  b[0] = *reinterpret_cast<const uint4*>(blk + o0 + 1024);
-  b[1] = *reinterpret_cast<const uint4*>(blk + o1 + 1024);
-  const uint32_t* aw = reinterpret_cast<const uint32_t*>(a);
-  const uint32_t* bw = reinterpret_cast<const uint32_t*>(b);
-  acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
 #pragma unroll
-  for (int ks = 0; ks < 8; ++ks)
-    mma_f16(acc, paged::e4m3x2_to_f16x2(aw[ks]), paged::e4m3x2_to_f16x2(bw[ks]),
-            paged::e4m3x2_hi_to_f16x2(aw[ks]), paged::e4m3x2_hi_to_f16x2(bw[ks]), bq[ks][0],
-            bq[ks][1]);
-}
-
-// out += vs * (2^14 P) V for the sixteen values whose rows lie at `blk` (swizzled as
-// above); s are their weights as packed by the score fragment's layout (keys r, r +
-// 8; heads 2 c, 2 c + 1); rows from `valid` on hold nothing and count as zero
-// whatever their bytes are. Rows r and r + 8 of m-block db stand for dimensions 16 r +
-// 2 db and 16 r + 2 db + 1, so that a thread's sixteen bytes of a value serve all eight
-// m-blocks.
-__device__ __forceinline__ void add_pv16(const unsigned char* blk, int valid, const float (&w)[4],
-                                         float vs, float (&out)[8][4]) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const uint32_t b0 = movmatrix_trans(pack_f16(w[0], w[1]));
-  const uint32_t b1 = movmatrix_trans(pack_f16(w[2], w[3]));
-  uint4 v[4];
+  for (int k = 0; k < TERMS; ++k) {
+    uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = 2 * c + (i & 1) + 8 * (i >> 1);
-    v[i] = *reinterpret_cast<const uint4*>(blk + key * 128 + ((r ^ (key & 7)) << 4));
-    if (key >= valid) v[i] = make_uint4(0, 0, 0, 0);
-  }
-  const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&v[0]);
-  const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&v[1]);
-  const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&v[2]);
-  const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&v[3]);
-#pragma unroll
-  for (int db = 0; db < 8; ++db) {
-    const uint32_t sel = (db & 1) ? 0x7362 : 0x5140;
-    const uint32_t lo = __byte_perm(w0[db >> 1], w1[db >> 1], sel);
-    const uint32_t hi = __byte_perm(w2[db >> 1], w3[db >> 1], sel);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    mma_f16(acc, paged::e4m3x2_to_f16x2(lo), paged::e4m3x2_hi_to_f16x2(lo),
-            paged::e4m3x2_to_f16x2(hi), paged::e4m3x2_hi_to_f16x2(hi), b0, b1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[db][i] = fmaf(acc[i], vs, out[db][i]);
+    for (int h = 0; h < 2; ++h) {
+      float* y = x + 4 * h;
+      w[h] = paged::floats_to_e4m3x2(y[0], y[1]) | paged::floats_to_e4m3x2(y[2], y[3]) << 16;
+      const float2 lo = paged::f16x2_to_float2(paged::e4m3x2_to_f16x2(w[h]));
+      const float2 hi = paged::f16x2_to_float2(paged::e4m3x2_hi_to_f16x2(w[h]));
+      y[0] = (y[0] - lo.x) * 16.f;
+      y[1] = (y[1] - lo.y) * 16.f;
+      y[2] = (y[2] - hi.x) * 16.f;
+      y[3] = (y[3] - hi.y) * 16.f;
+    }
+    const int n = k * GH + g;
+    *reinterpret_cast<uint2*>(sh.q + n * 128 + (((c >> 1) ^ (n & 7)) << 4) + (c & 1) * 8) =
+        make_uint2(w[0], w[1]);
   }
 }
 
-// What the blocks of a cluster hold beside their rings.
-struct Shared {
-  uint64_t full[NW][3];
-  uint64_t pv[NW];
-  float mfin[GMAX], lfin[GMAX];  // final max (log2 units) and mass
-  float wm[NW][GMAX], wl[NW][GMAX];
-  int bad, abort, items;
-};
-
-// The group's place, common to both kernels.
-struct Group {
-  int b, h, len, nt;
-  long long grp;
-};
-
-// The pages of a chunk's 32 positions: one, or two of 16 tokens. -1: none needed or
-// no page of the pool (then *bad is set).
-__device__ __forceinline__ void chunk_pages(const Pool& pool, int b, int pos, int len, int& id0,
-                                            int& id1, int* bad) {
-  id0 = id1 = -1;
-  if (pos >= len) return;
-  const int slot = pos >> pool.page_log2;
-  id0 = paged::page_of(pool, b, slot);
-  if (id0 < 0) *bad = 1;
-  if (pool.page == 16 && pos + 16 < len) {
-    id1 = paged::page_of(pool, b, slot + 1);
-    if (id1 < 0) *bad = 1;
-  }
-}
-
-// Lane 0: loads the 32 rows from position `pos` into `dst`, counted on `bar`
-// (which the caller arms with chunk_bytes).
-__device__ __forceinline__ void load_chunk(const CUtensorMap* map, const Pool& pool, uint32_t dst,
-                                           int pos, int h, int id0, int id1, uint32_t bar) {
-  if (id0 >= 0) sm100::tma_load_4d(dst, map, 0, pos & (pool.page - 1), h, id0, bar);
-  if (id1 >= 0) sm100::tma_load_4d(dst + STAGE / 2, map, 0, 0, h, id1, bar);
-}
-__device__ __forceinline__ uint32_t chunk_bytes(const Pool& pool, int id0, int id1) {
-  if (pool.page != 16) return id0 >= 0 ? STAGE : 0;
-  return (id0 >= 0 ? STAGE / 2 : 0) + (id1 >= 0 ? STAGE / 2 : 0);
-}
-
-// Scores of a chunk in log2 units, -inf where there is no key (behind the
-// sequence, or in a page that is not in the pool).
-__device__ __forceinline__ void chunk_scores(const unsigned char* stage, const uint32_t (&bq)[8][2],
-                                             int pos, int len, bool has0, bool has1, float f00,
-                                             float f01, float f10, float f11, float (&s)[2][4]) {
-  const int r = (threadIdx.x & 31) >> 2;
-  scores16(stage, bq, s[0]);
-  scores16(stage + 2048, bq, s[1]);
-  s[0][0] *= f00;
-  s[0][1] *= f01;
-  s[0][2] *= f00;
-  s[0][3] *= f01;
-  s[1][0] *= f10;
-  s[1][1] *= f11;
-  s[1][2] *= f10;
-  s[1][3] *= f11;
-  if (pos + CK > len || !has0 || !has1) {
+// The four terms' columns of a row joined, per head.
+template <int GH>
+__device__ __forceinline__ void join_terms(const float (&v)[TERMS * GH], float (&x)[GH]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool has = i ? has1 : has0;
-      if (!has || pos + 16 * i + r >= len) s[i][0] = s[i][1] = kNegInf;
-      if (!has || pos + 16 * i + r + 8 >= len) s[i][2] = s[i][3] = kNegInf;
+  for (int g = 0; g < GH; ++g)
+    x[g] = fmaf(fmaf(fmaf(v[3 * GH + g], 1.f / 16.f, v[2 * GH + g]), 1.f / 16.f, v[GH + g]),
+                1.f / 16.f, v[g]);
+}
+
+// A key's probabilities (scaled by 2^8) as e4m3 terms into its row of P.
+template <int GH>
+__device__ __forceinline__ void store_p(unsigned char* buf, int key, const float (&p)[GH]) {
+  uint32_t w[TERMS][GH / 4];
+  const __half2 up = __float2half2_rn(16.f), down = __float2half2_rn(-16.f);
+#pragma unroll
+  for (int j = 0; j < GH / 2; ++j) {
+    __half2 h = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) {
+      const uint32_t t = f16x2_to_e4m3x2(h);
+      w[k][j / 2] = (j & 1) ? w[k][j / 2] | t << 16 : t;
+      if (k + 1 < TERMS) h = __hfma2(e4m3x2_to_half2(t), down, __hmul2(h, up));
     }
   }
+  const uint32_t* x = &w[0][0];
+#pragma unroll
+  for (int n = 0; n < TERMS * GH / 16; ++n)
+    *reinterpret_cast<uint4*>(buf + n * (T * 16) + key * 16) =
+        make_uint4(x[4 * n], x[4 * n + 1], x[4 * n + 2], x[4 * n + 3]);
 }
 
-// Joins the warps' and the blocks' outputs (each scaled to the same reference)
-// and writes o = sum / (2^14 l).
-__device__ __forceinline__ void join_and_store(const Params& p, Shared& sh, float* part,
-                                               const float (&out)[8][4], const float* wscale,
-                                               uint32_t rank, __nv_bfloat16* o, bool dense) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
-  const int n = p.G * D;
-  __syncthreads();  // the rings are free
-  float* mine = part + warp * (GMAX * D);
-#pragma unroll
-  for (int db = 0; db < 8; ++db)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float2*>(mine + (2 * c + i) * D + 16 * r + 2 * db) =
-          make_float2(out[db][i] * wscale[i], out[db][2 + i] * wscale[i]);
-  __syncthreads();
-  for (int e = tid; e < n; e += NT) {
-    float x = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) x += part[w * (GMAX * D) + e];
-    part[e] = x;
+// The load warp: tiles one after the other into the ring. `place(i)`: the i-th tile's first
+// position and heads. With values, a tile's V follows its K. `seq`: stages used so far.
+template <typename Sh, typename Place>
+__device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* tmK,
+                                           const CUtensorMap* tmV, unsigned char* ring, Sh& sh,
+                                           int b, int h, int len, int tiles, bool values,
+                                           uint32_t seq, uint32_t meta0, Place place) {
+  const int lane = threadIdx.x & 31;
+  const int per_log2 = 7 - pool.page_log2, per = 1 << per_log2;  // pages of a tile
+  const int batch = 32 >> per_log2, sub = lane & (per - 1);
+  const int32_t* row = pool.table + (long long)b * pool.table_stride;
+  volatile int* abort = &sh.abort;
+  for (int i0 = 0; i0 < tiles; i0 += batch) {
+    // 32 pages at a time, a lane each
+    const int i = i0 + (lane >> per_log2);
+    int pos = 0, id = -1;
+    uint32_t heads = 0;
+    float ks = 0.f, vs = 0.f;
+    if (i < tiles) {
+      place(i, pos, heads);
+      const int at = pos + sub * pool.page, slot = at >> pool.page_log2;
+      if (at < len) {
+        if (slot < pool.max_pages) id = row[slot];
+        if ((unsigned)id >= (unsigned)pool.num_pages) {
+          record_bad_page(0x500);
+          sh.bad = 1;
+          id = -1;
+        }
+      }
+      if (id >= 0) {
+        ks = pool.k_scale[(long long)id * pool.Hkv + h];
+        if (values) vs = pool.v_scale[(long long)id * pool.Hkv + h];
+      }
+    }
+    const int n = min(batch, tiles - i0);
+    for (int j = 0; j < n; ++j) {
+      const bool mine = (lane >> per_log2) == j;
+      const uint32_t bytes =
+          (uint32_t)__popc(__ballot_sync(0xffffffffu, mine && id >= 0)) * (uint32_t)pool.page * D;
+      for (int w = 0; w < (values ? 2 : 1); ++w, ++seq) {
+        const uint32_t st = seq % NST, turn = seq / NST;
+        bool ok = true;
+        if (lane == 0 && turn > 0)
+          ok = mbar_wait(smem_u32(&sh.empty[st]), (turn - 1) & 1, abort, 0x511);
+        if (!__shfl_sync(0xffffffffu, (int)ok, 0)) return false;
+        if (mine && w == 0) {  // sixteen tiles are held, the softmax is eight behind at most
+          Meta& m = sh.meta[(meta0 + (uint32_t)(i0 + j)) % NMETA];
+          if (sub == 0) {
+            m.pos = pos;
+            m.heads = heads;
+          }
+          for (int u = 0; u < (8 >> per_log2); ++u) {
+            m.k[(sub << (3 - per_log2)) + u] = ks;
+            m.v[(sub << (3 - per_log2)) + u] = vs;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(smem_u32(&sh.full[st]), bytes);
+        __syncwarp();
+        if (mine && id >= 0)
+          sm100::tma_load_4d(smem_u32(ring) + st * TILE_BYTES + (uint32_t)(sub * pool.page) * D,
+                             w ? tmV : tmK, 0, 0, h, id, smem_u32(&sh.full[st]));
+      }
+    }
   }
+  return true;
+}
+
+// One thread issues the products. S of the tile in ring stage `seq` into S buffer s & 1:
+template <int GH>
+__device__ __forceinline__ bool issue_s(Shared<GH>& sh, unsigned char* ring, uint32_t seq,
+                                        uint32_t s) {
+  constexpr uint32_t ID = idesc_e4m3(T, TERMS * GH, false, false);
+  volatile int* abort = &sh.abort;
+  const uint32_t st = seq % NST, buf = s & 1;
+  if (!mbar_wait(smem_u32(&sh.full[st]), (seq / NST) & 1, abort, 0x512)) return false;
+  if (s >= 2 && !mbar_wait(smem_u32(&sh.s_empty[buf]), ((s >> 1) - 1) & 1, abort, 0x513))
+    return false;
+  sm100::tc_fence_after();
+  const uint64_t a = sm100::sdesc_sw128(smem_u32(ring) + st * TILE_BYTES, 16, 1024);
+  const uint64_t b = sm100::sdesc_sw128(smem_u32(sh.q), 16, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+    mma_e4m3(sh.tmem + buf * (TERMS * GH), a + 2 * kk, b + 2 * kk, ID, kk > 0);
+  sm100::mma_commit(smem_u32(&sh.empty[st]));
+  sm100::mma_commit(smem_u32(&sh.s_full[buf]));
+  return true;
+}
+// O of the i-th tile with values, V in ring stage `seq`:
+template <int GH>
+__device__ __forceinline__ bool issue_o(Shared<GH>& sh, unsigned char* ring, uint32_t seq,
+                                        uint32_t i) {
+  constexpr uint32_t ID = idesc_e4m3(T, TERMS * GH, true, true);
+  volatile int* abort = &sh.abort;
+  const uint32_t st = seq % NST, buf = i & 1;
+  if (!mbar_wait(smem_u32(&sh.p_full[buf]), (i >> 1) & 1, abort, 0x514)) return false;
+  if (!mbar_wait(smem_u32(&sh.full[st]), (seq / NST) & 1, abort, 0x515)) return false;
+  if (i >= 2 && !mbar_wait(smem_u32(&sh.o_empty[buf]), ((i >> 1) - 1) & 1, abort, 0x516))
+    return false;
+  sm100::tc_fence_after();
+  const uint64_t a = sm100::sdesc_sw128(smem_u32(ring) + st * TILE_BYTES, TILE_BYTES, 1024);
+  const uint64_t b = sdesc_plain(smem_u32(sh.p[buf]), 128, T * 16);
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4 KB of V, 512 bytes of P
+    mma_e4m3(sh.tmem + (2 + buf) * (TERMS * GH), a + 256 * kk, b + 32 * kk, ID, kk > 0);
+  sm100::mma_commit(smem_u32(&sh.empty[st]));
+  sm100::mma_commit(smem_u32(&sh.o_full[buf]));
+  return true;
+}
+
+// A softmax warp's wait. When it runs out the warp goes on all the same, over whatever lies
+// there: the others wait for it at their barriers, and the call is reported as timed out.
+__device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, int* abort,
+                                          unsigned where) {
+  mbar_wait(smem_u32(bar), parity, abort, where);
+  __syncwarp();
+}
+
+// A softmax warp is through with a buffer.
+__device__ __forceinline__ void release(uint64_t* bar) {
+  sm100::tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+}
+
+// Scores of this thread's key in log2 units, -inf behind the sequence; S buffer s & 1 (whose
+// barrier the caller waited for) is given back. What the caller wants of m is read before: the
+// load warp may overwrite it later.
+template <int GH>
+__device__ __forceinline__ void scores(Shared<GH>& sh, uint32_t s, const Meta& m, int len,
+                                       const float (&undo)[GH], float (&x)[GH]) {
+  const int key = threadIdx.x;
+  const uint32_t buf = s & 1;
+  sm100::tc_fence_after();
+  float v[TERMS * GH];
+  tmem_ld(sh.tmem + buf * (TERMS * GH) + ((uint32_t)(key >> 5) << 21), v);
+  const float ks = m.k[key >> 4];
+  const bool in = key < len - m.pos;
+  release(&sh.s_empty[buf]);
+  join_terms<GH>(v, x);
+#pragma unroll
+  for (int g = 0; g < GH; ++g) x[g] = in ? x[g] * (undo[g] * ks) : kNegInf;
+}
+
+// out += O of the i-th tile, f[g] times, for the heads that keep it (a value that is NaN
+// shows only in those).
+template <int GH>
+__device__ __forceinline__ void add_o(Shared<GH>& sh, uint32_t i, const float (&f)[GH],
+                                      uint32_t heads, float (&out)[GH]) {
+  const uint32_t buf = i & 1;
+  warp_wait(&sh.o_full[buf], (i >> 1) & 1, &sh.abort, 0x518);
+  sm100::tc_fence_after();
+  float v[TERMS * GH];
+  tmem_ld(sh.tmem + (2 + buf) * (TERMS * GH) + ((threadIdx.x >> 5) << 21), v);
+  release(&sh.o_empty[buf]);
+  float x[GH];
+  join_terms<GH>(v, x);
+#pragma unroll
+  for (int g = 0; g < GH; ++g)
+    if ((heads >> g) & 1u) out[g] = fmaf(x[g], f[g], out[g]);
+}
+
+// The softmax threads' part of the tiles with values. FIXED: `mref` is the rows' final
+// max; else it runs along, and l is the mass of this thread's keys.
+template <int GH, bool FIXED>
+__device__ __forceinline__ void softmax_pv(Shared<GH>& sh, unsigned char* ring, int len, int tiles,
+                                           uint32_t s0, uint32_t seq0, const float (&undo)[GH],
+                                           float (&mref)[GH], float (&l)[GH], float (&out)[GH]) {
+  const int key = threadIdx.x, warp = key >> 5;
+  float f[GH];  // the tile before: what its O counts
+#pragma unroll
+  for (int g = 0; g < GH; ++g) f[g] = 0.f;
+  uint32_t heads_before = 0;
+  for (int i = 0; i < tiles; ++i) {
+    const Meta& m = sh.meta[(s0 + (uint32_t)i) % NMETA];
+    const uint32_t s = s0 + (uint32_t)i;
+    warp_wait(&sh.s_full[s & 1], (s >> 1) & 1, &sh.abort, 0x517);
+    const int left = len - m.pos;
+    const uint32_t heads = FIXED ? m.heads : 0xffu;
+    // pages of different scales: V's bytes count u, the largest, and P takes the rest
+    const float4 v0 = *reinterpret_cast<const float4*>(m.v);
+    const float4 v1 = *reinterpret_cast<const float4*>(m.v + 4);
+    const float vs = m.v[key >> 4];
+    const float u = fmaxf(fmaxf(fmaxf(fabsf(v0.x), fabsf(v0.y)), fmaxf(fabsf(v0.z), fabsf(v0.w))),
+                          fmaxf(fmaxf(fabsf(v1.x), fabsf(v1.y)), fmaxf(fabsf(v1.z), fabsf(v1.w))));
+    const float ratio = vs == u ? 1.f : (vs == 0.f ? 0.f : vs / u);
+    float x[GH];
+    scores<GH>(sh, s, m, len, undo, x);
+    if (!FIXED) {
+      bool above = false;
+#pragma unroll
+      for (int g = 0; g < GH; ++g) above |= x[g] > mref[g];
+      if (any_of_softmax(above)) {
+#pragma unroll
+        for (int g = 0; g < GH; ++g) {
+          const float top = warp_max(x[g]);
+          if ((key & 31) == 0) sh.wm[warp][g] = top;
+        }
+        sync_softmax();
+#pragma unroll
+        for (int g = 0; g < GH; ++g) {
+          const float top = fmaxf(fmaxf(sh.wm[0][g], sh.wm[1][g]), fmaxf(sh.wm[2][g], sh.wm[3][g]));
+          const float now = fmaxf(mref[g], top);
+          const float c = mref[g] == kNegInf ? 0.f : ex2_approx(mref[g] - now);
+          mref[g] = now;
+          l[g] *= c;
+          out[g] *= c;
+          f[g] *= c;
+        }
+      }
+    }
+    float p[GH];
+#pragma unroll
+    for (int g = 0; g < GH; ++g) {
+      if (FIXED && !((heads >> g) & 1u)) x[g] = kNegInf;
+      const float z = (mref[g] == kNegInf ? 0.f : mref[g]) - 8.f;
+      p[g] = ex2_approx(x[g] - z);
+      if (!FIXED) l[g] += p[g];
+      p[g] *= ratio;
+    }
+    store_p<GH>(sh.p[i & 1], key, p);
+    if (left < T) {
+      // rows behind the sequence hold anything, and a product with a NaN is NaN even where P
+      // is zero
+      const uint32_t seq = seq0 + 2u * (uint32_t)i + 1u, st = seq % NST;
+      warp_wait(&sh.full[st], (seq / NST) & 1, &sh.abort, 0x519);
+      if (key >= left)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          reinterpret_cast<uint4*>(ring + st * TILE_BYTES + key * D)[e] = make_uint4(0, 0, 0, 0);
+    }
+    sm100::fence_proxy_async_smem();
+    __syncwarp();
+    if ((key & 31) == 0) mbar_arrive(smem_u32(&sh.p_full[i & 1]));
+    if (i > 0) add_o<GH>(sh, i - 1, f, heads_before, out);
+    heads_before = heads;
+#pragma unroll
+    for (int g = 0; g < GH; ++g) f[g] = u * (1.f / 256.f);
+  }
+  if (tiles > 0) add_o<GH>(sh, tiles - 1, f, heads_before, out);
+}
+
+// Joins the blocks' outputs and writes o = sum / l: thread tid of the softmax warps has
+// dimension tid of every head. dense: the blocks' references differ (sh.mfin), else
+// sh.lfin is the whole cluster's mass. Each block owns some of the dimensions, and the others
+// write their partial sums of them into its shared memory: no round trips.
+template <int GH>
+__device__ __forceinline__ void join_and_store(const Params& p, Shared<GH>& sh, Join& jn,
+                                               const float (&out)[GH], uint32_t rank,
+                                               __nv_bfloat16* o, bool dense) {
+  const int tid = threadIdx.x, C = p.C, G = p.G;
   const float nan = __int_as_float(0x7fc00000);
-  if (p.C == 1) {
-    for (int e = tid; e < n; e += NT)
-      o[e] = __float2bfloat16_rn(sh.bad ? nan : part[e] / (sh.lfin[e / D] * 16384.f));
+  if (C == 1) {
+    if (tid < NC)
+#pragma unroll
+      for (int g = 0; g < GH; ++g)
+        if (g < G) o[g * D + tid] = __float2bfloat16_rn(sh.bad ? nan : out[g] / sh.lfin[g]);
     return;
   }
-  sm100::cluster_sync_all();
-  const int each = (n + p.C - 1) >> p.C_log2;
-  const uint32_t part_a = smem_u32(part), bad_a = smem_u32(&sh.bad), m_a = smem_u32(sh.mfin),
-                 l_a = smem_u32(sh.lfin);
-  for (int i = tid; i < each; i += NT) {
-    const int e = (int)rank * each + i;
-    if (e >= n) break;
-    float x = 0.f, l = 0.f, top = kNegInf;
+  cluster_arrive();  // the ring is free, and may be written to by the other blocks
+  cluster_wait();
+  const int each = (D + C - 1) / C;  // dimensions a block owns
+  if (tid < NC) {
+    const int owner = tid / each, i = tid - owner * each;
+#pragma unroll
+    for (int g = 0; g < GH; ++g)
+      if (g < G)
+        sm100::st_cluster_f32(sm100::mapa_rank(smem_u32(&jn.recv[((int)rank * G + g) * each + i]), owner), out[g]);
+  } else if (tid < NC + C) {
+    sm100::st_cluster_u32(sm100::mapa_rank(smem_u32(&jn.bad[rank]), tid - NC), sh.bad);
+  }
+  if (dense && tid < GMAX * C) {
+    const int g = tid % GMAX;
+    sm100::st_cluster_f32x2(sm100::mapa_rank(smem_u32(&jn.ml[rank][g]), tid / GMAX),
+                            make_float2(sh.mfin[g], sh.lfin[g]));
+  }
+  cluster_arrive();
+  cluster_wait();
+  for (int e = tid; e < G * each; e += NT) {
+    const int g = e / each, i = e - g * each, dim = (int)rank * each + i;
+    if (dim >= D) continue;
+    float sum = 0.f, l = dense ? 0.f : sh.lfin[g], top = kNegInf;
     int bad = 0;
-    const int g = e / D;
     if (dense)
-      for (int k = 0; k < p.C; ++k)
-        top = fmaxf(top, sm100::ld_cluster_f32(sm100::mapa_rank(m_a + 4 * g, k)));
-    for (int k = 0; k < p.C; ++k) {
+      for (int k = 0; k < C; ++k) top = fmaxf(top, jn.ml[k][g].x);
+    for (int k = 0; k < C; ++k) {
       float f = 1.f;
       if (dense) {
-        const float m = sm100::ld_cluster_f32(sm100::mapa_rank(m_a + 4 * g, k));
-        f = m == kNegInf ? 0.f : ex2_approx(m - top);
-        l += f * sm100::ld_cluster_f32(sm100::mapa_rank(l_a + 4 * g, k));
+        const float2 ml = jn.ml[k][g];
+        f = ml.x == kNegInf ? 0.f : ex2_approx(ml.x - top);
+        l += f * ml.y;
       }
-      x += f * sm100::ld_cluster_f32(sm100::mapa_rank(part_a + 4 * e, k));
-      bad |= (int)sm100::ld_cluster_u32(sm100::mapa_rank(bad_a, k));
+      sum += f * jn.recv[k * G * each + e];
+      bad |= jn.bad[k];
     }
-    if (!dense) l = sh.lfin[g];
-    o[e] = __float2bfloat16_rn(bad ? nan : x / (l * 16384.f));
+    o[g * D + dim] = __float2bfloat16_rn(bad ? nan : sum / l);
   }
-  __syncwarp();
-  sm100::cluster_sync_all();  // no block's shared memory goes while others read it
 }
 
 // An unused slot of the batch, or a length that the call did not allow for:
 // the output without any work. True when there is nothing else to do.
-__device__ __forceinline__ bool trivial(const Params& p, const Group& g, uint32_t rank,
+__device__ __forceinline__ bool trivial(const Params& p, long long grp, int len, uint32_t rank,
                                         __nv_bfloat16* o) {
-  const bool fits = g.nt <= p.max_tiles;
-  if (g.nt > 0 && fits) return false;
+  const bool fits = len <= p.max_len;
+  if (len > 0 && fits) return false;
   if (rank == 0) {
     const int tid = threadIdx.x, units = p.per_head ? p.G : 1;
     if (!fits && tid == 0) record_bad_page(0x510);
     const __nv_bfloat16 z = __float2bfloat16_rn(fits ? 0.f : __int_as_float(0x7fc00000));
     for (int e = tid; e < p.G * D; e += NT) o[e] = z;
-    if (p.kept_tiles && tid < units) p.kept_tiles[g.grp * units + tid] = 0;
+    if (p.kept_tiles && tid < units) p.kept_tiles[grp * units + tid] = 0;
     if (p.keep_bits)
-      for (int e = tid; e < units * p.nw; e += NT) p.keep_bits[g.grp * units * p.nw + e] = 0u;
+      for (int e = tid; e < units * p.nw; e += NT) p.keep_bits[grp * units * p.nw + e] = 0u;
   }
   return true;
 }
 
-__device__ __forceinline__ Group group_of(const Params& p) {
-  Group g;
-  g.h = blockIdx.y;
-  g.b = blockIdx.z;
-  g.len = p.seq_lens[g.b];
-  g.nt = g.len > 0 ? (int)(((long long)g.len + T - 1) / T) : 0;
-  g.grp = (long long)g.b * p.Hkv + g.h;
-  return g;
-}
+// A head's running max and mass over the kept tiles, and the least tile max that is kept.
+struct Walk {
+  float m, l, bound;
+  __device__ __forceinline__ void take(float2 s, float thr) {
+    const float mn = fmaxf(m, s.x);
+    const float z = mn == kNegInf ? 0.f : mn;
+    l = l * ex2_approx(m - z) + s.y * ex2_approx(s.x - z);
+    m = mn;
+    bound = mn + lg2_approx(l) + thr;
+  }
+};
 
-// Statistics slots of a block: its warps' tiles, slot i * NW + warp the warp's i-th.
-__host__ __device__ inline int rule_slots(int max_tiles, int C) {
-  return (max_tiles + NW * C - 1) / (NW * C) * NW;
-}
-inline size_t rule_smem(int G, int max_tiles, int C) {
-  return 1024 + RULE_RING + (size_t)rule_slots(max_tiles, C) * (G * sizeof(float2)) +
-         ((size_t)(max_tiles + C - 1) / C) * sizeof(uint32_t);
-}
-constexpr size_t DENSE_SMEM = 1024 + DENSE_RING;
-
-__global__ void __launch_bounds__(NT, 2) rule_kernel(const __grid_constant__ CUtensorMap tmK,
-                                                     const __grid_constant__ CUtensorMap tmV,
-                                                     const Params p) {
-  extern __shared__ unsigned char raw[];
-  __shared__ Shared sh;
-  unsigned char* ring = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+// Phase B: replays the rule over the cluster's statistics, newest first, in stretches that
+// fit in the ring's space (a single block's statistics lie in tile order already); leaves the
+// rows' final max and mass, the keep bits, and this block's list of tiles. Group: one warp,
+// lane = (head, tile mod 4), 32 tiles at a time in registers; a kept tile costs one look-up
+// and one update, all heads at once. Per head: a warp per head, lane = tile.
+template <int GH>
+__device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, unsigned char* smem,
+                                            float2* stats, uint32_t* keep, uint32_t* list,
+                                            long long grp, int len, int nt, uint32_t rank) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c = lane & 3;
-  const int G = p.G, C = p.C;
-  const Pool& pool = p.pool;
-  const uint32_t rank = blockIdx.x;
-  const Group gr = group_of(p);
-  const int len = gr.len, nt = gr.nt;
-  __nv_bfloat16* o = p.o + gr.grp * G * D;
-  if (trivial(p, gr, rank, o)) return;
-
-  const int slots = rule_slots(p.max_tiles, C);
-  float2* stats = reinterpret_cast<float2*>(ring + RULE_RING);               // [G][slots]
-  uint32_t* list = reinterpret_cast<uint32_t*>(stats + (size_t)G * slots);   // this block's items
-  if (tid == 0) {
-    for (int w = 0; w < NW; ++w) {
-      for (int s = 0; s < RULE_NST; ++s) sm100::mbar_init(smem_u32(&sh.full[w][s]), 1);
-      sm100::mbar_init(smem_u32(&sh.pv[w]), 1);
-    }
-    sh.bad = sh.abort = sh.items = 0;
-    sm100::fence_mbar_init();
-  }
-  const int units = p.per_head ? G : 1;
-  if (rank == 0 && p.keep_bits)
-    for (int e = tid; e < units * p.nw; e += NT) p.keep_bits[gr.grp * units * p.nw + e] = 0u;
-  __syncthreads();
-  volatile int* abort = &sh.abort;
-
-  uint32_t bq[8][2];
-  const float undo = load_q(p.q + gr.grp * G * D, G, bq) * p.scale_log2;
-  const float undo0 = __shfl_sync(0xffffffffu, undo, 8 * c);      // head 2 c
-  const float undo1 = __shfl_sync(0xffffffffu, undo, 8 * c + 4);  // head 2 c + 1
-
-  // ---- A: statistics of this warp's tiles, a ring of chunks
-  unsigned char* my = ring + warp * (RULE_NST * STAGE);
-  const int W = NW * C, wg = (int)rank * NW + warp;
-  const int tiles = nt > wg ? (nt - wg + W - 1) / W : 0, chunks = 4 * tiles;
-  auto pos_of = [&](int k) { return (wg + (k >> 2) * W) * T + (k & 3) * CK; };
-  // pages and scales of 32 chunks at a time, lane i those of the i-th; the next 32
-  // are fetched while these are in use
-  int id0, id1, nid0 = -1, nid1 = -1;
-  float sc0 = 0.f, sc1 = 0.f, nsc0 = 0.f, nsc1 = 0.f;
-  auto fetch_ids = [&](int k, int& a, int& b) {
-    a = b = -1;
-    if (k < chunks) chunk_pages(pool, gr.b, pos_of(k), len, a, b, &sh.bad);
-  };
-  auto fetch_scales = [&](int a, int b, float& x, float& y) {
-    x = a >= 0 ? pool.k_scale[(long long)a * pool.Hkv + gr.h] : 0.f;
-    y = b >= 0 ? pool.k_scale[(long long)b * pool.Hkv + gr.h] : x;
-  };
-  auto issue = [&](int k, int a, int b) {  // warp-uniform
-    if (lane == 0) {
-      const int s = k % RULE_NST;
-      const uint32_t bar = smem_u32(&sh.full[warp][s]);
-      mbar_expect_tx(bar, chunk_bytes(pool, a, b));
-      load_chunk(&tmK, pool, smem_u32(my + s * STAGE), pos_of(k), gr.h, a, b, bar);
-    }
-  };
-  fetch_ids(lane, id0, id1);
+  const int G = p.G, GP = p.GP, C = p.C;
+  const int units = p.per_head ? G : 1, words = rule_words(p.max_tiles);
+  const float2* loc = C > 1 ? reinterpret_cast<const float2*>(smem) : stats;
+  const int cap = C > 1 ? ((int)(RING / sizeof(float2)) / GP) & ~31 : 0x7fffffe0;
+  const uint32_t stats_a = smem_u32(stats);
+  const float thr = p.log2_tau - lg2_approx((float)len);
+  Walk w = {kNegInf, 0.f, kNegInf};
+  for (int hi = nt; hi > 0;) {
+    const int lo = hi > cap ? (hi - cap + 31) & ~31 : 0;
+    if (C > 1) {
+      const int per = GP / 2, n = (hi - lo) * per;  // pieces of sixteen bytes
+      for (int e0 = tid; e0 < n; e0 += 4 * NT) {
+        float4 x[4];
 #pragma unroll
-  for (int k = 0; k < RULE_NST; ++k) {
-    const int a = __shfl_sync(0xffffffffu, id0, k), b = __shfl_sync(0xffffffffu, id1, k);
-    if (k < chunks) issue(k, a, b);
-  }
-  fetch_scales(id0, id1, sc0, sc1);
-  bool ok = true;
-  int stage = 0;
-  uint32_t phase = 0;
-  for (int i = 0; i < tiles && ok; ++i) {
-    if ((i & 7) == 0) {
-      if (i > 0) {
-        id0 = nid0;
-        id1 = nid1;
-        sc0 = nsc0;
-        sc1 = nsc1;
-      }
-      fetch_ids(4 * i + 32 + lane, nid0, nid1);
-    } else if ((i & 7) == 4) {
-      fetch_scales(nid0, nid1, nsc0, nsc1);
-    }
-    float s[8][4];
-#pragma unroll
-    for (int qr = 0; qr < 4; ++qr) {
-      const int k = 4 * i + qr, j = k & 31;
-      const int a = __shfl_sync(0xffffffffu, id0, j), b = __shfl_sync(0xffffffffu, id1, j);
-      const float x = __shfl_sync(0xffffffffu, sc0, j), y = __shfl_sync(0xffffffffu, sc1, j);
-      ok = __all_sync(0xffffffffu,
-                      ok && mbar_wait(smem_u32(&sh.full[warp][stage]), phase, abort, 0x511));
-      float t2[2][4];
-      chunk_scores(my + stage * STAGE, bq, pos_of(k), len, a >= 0, pool.page == 16 ? b >= 0 : a >= 0,
-                   undo0 * x, undo1 * x, undo0 * y, undo1 * y, t2);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[2 * qr][e] = t2[0][e];
-        s[2 * qr + 1][e] = t2[1][e];
-      }
-      const int nk = k + RULE_NST, nj = nk & 31;
-      const bool next = (nk >> 5) != (k >> 5);
-      const int na = __shfl_sync(0xffffffffu, next ? nid0 : id0, nj);
-      const int nb = __shfl_sync(0xffffffffu, next ? nid1 : id1, nj);
-      __syncwarp();  // every lane has read the stage
-      if (nk < chunks && ok) issue(nk, na, nb);
-      if (++stage == RULE_NST) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
-    float m0 = kNegInf, m1 = kNegInf;
-#pragma unroll
-    for (int kb = 0; kb < 8; ++kb) {
-      m0 = fmaxf(m0, fmaxf(s[kb][0], s[kb][2]));
-      m1 = fmaxf(m1, fmaxf(s[kb][1], s[kb][3]));
-    }
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) {
-      m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
-      m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
-    }
-    // a tile without a finite score: mass 0
-    const float z0 = m0 == kNegInf ? 0.f : m0, z1 = m1 == kNegInf ? 0.f : m1;
-    float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < 8; ++kb) {
-      l0 += ex2_approx(s[kb][0] - z0) + ex2_approx(s[kb][2] - z0);
-      l1 += ex2_approx(s[kb][1] - z1) + ex2_approx(s[kb][3] - z1);
-    }
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-    }
-    if (isnan(l0)) m0 = l0;  // a tile with a NaN score is kept, and shows
-    if (isnan(l1)) m1 = l1;
-    if (lane < 4) {
-      if (2 * c < G) stats[2 * c * slots + i * NW + warp] = make_float2(m0, l0);
-      if (2 * c + 1 < G) stats[(2 * c + 1) * slots + i * NW + warp] = make_float2(m1, l1);
-    }
-  }
-  if (!ok) sm100::drain_in_flight();
-  __syncwarp();
-  if (C > 1)
-    sm100::cluster_sync_all();
-  else
-    __syncthreads();
-
-  // ---- B: the rule over all tiles, newest first, in stretches that fit in the
-  // ring's space (a single block's statistics lie in tile order already)
-  {
-    float2* loc = C > 1 ? reinterpret_cast<float2*>(ring) : stats;
-    const int cap = C > 1 ? ((int)(RULE_RING / sizeof(float2)) / G) & ~31 : slots;
-    const uint32_t stats_a = smem_u32(stats);
-    const float thr = p.log2_tau - lg2_approx((float)len);
-    const uint32_t all = (1u << G) - 1u;
-    float m[GMAX], l[GMAX], bound[GMAX];
-    int cnt[GMAX];
-    int count = 0, next = nt - 1;
-#pragma unroll
-    for (int g = 0; g < GMAX; ++g) {
-      m[g] = kNegInf;
-      l[g] = 0.f;
-      cnt[g] = 0;
-      bound[g] = kNegInf;
-    }
-    for (int hi = nt; hi > 0;) {
-      const int lo = C > 1 ? max(0, hi - cap) : 0;
-      if (C > 1) {
-        const int n = hi - lo;
-        for (int g = 0; g < G; ++g)
-          for (int e = tid; e < n; e += NT) {
-            const int t = lo + e, w = t & (W - 1);
-            const uint32_t at = stats_a + 8u * (uint32_t)(g * slots + (t / W) * NW + (w & (NW - 1)));
-            loc[g * cap + e] = sm100::ld_cluster_f32x2(sm100::mapa_rank(at, w / NW));
-          }
-        __syncthreads();
-      }
-      if (warp == 0) {
-        auto take = [&](int t, uint32_t hm) {
-#pragma unroll
-          for (int g = 0; g < GMAX; ++g) {
-            if (!((hm >> g) & 1u)) continue;
-            const float2 s = loc[g * cap + t - lo];
-            const float mn = fmaxf(m[g], s.x);
-            const float z = mn == kNegInf ? 0.f : mn;
-            l[g] = l[g] * ex2_approx(m[g] - z) + s.y * ex2_approx(s.x - z);
-            m[g] = mn;
-            bound[g] = mn + lg2_approx(l[g]) + thr;
-            ++cnt[g];
-            if (p.keep_bits && rank == 0 && lane == 0 && (p.per_head || g == 0))
-              p.keep_bits[(gr.grp * units + (p.per_head ? g : 0)) * p.nw + (t >> 5)] |= 1u << (t & 31);
-          }
-          if (lane == 0 && (count & (C - 1)) == (int)rank) list[count >> p.C_log2] = (uint32_t)t | hm << 24;
-          ++count;
-        };
-        if (next == nt - 1) {
-          take(next, all);
-          --next;
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + u * NT;
+          if (e >= n) break;
+          const int t = lo + e / per, slot = t / C;
+          x[u] = sm100::ld_cluster_f32x4(sm100::mapa_rank(
+              stats_a + 16u * (uint32_t)(slot * per + e % per), (uint32_t)(t - slot * C)));
         }
-        while (next >= lo) {
-          const int t = next - lane;
-          uint32_t want = 0;
-          if (t >= lo) {
 #pragma unroll
-            for (int g = 0; g < GMAX; ++g)  // a NaN keeps
-              if (g < G && !(loc[g * cap + t - lo].x < bound[g])) want |= 1u << g;
-            if (!p.per_head && want) want = all;
-          }
-          const unsigned vote = __ballot_sync(0xffffffffu, want != 0u);
-          if (!vote) {
-            next -= 32;
-            continue;
-          }
-          const int src = __ffs(vote) - 1;
-          take(next - src, __shfl_sync(0xffffffffu, want, src));
-          next -= src + 1;
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + u * NT;
+          if (e < n) reinterpret_cast<float4*>(smem)[e] = x[u];
         }
-        next = lo - 1;
       }
-      hi = lo;
-      if (hi > 0) __syncthreads();
+      __syncwarp();
+      __syncthreads();
     }
-    if (warp == 0) {
-      if (lane == 0) sh.items = (count - (int)rank + C - 1) >> p.C_log2;
+    if (p.per_head ? warp < G : warp == 0) {
+      for (int wi = (hi - 1) >> 5; wi >= lo >> 5; --wi) {
+        const float2* at = loc + (size_t)(wi * 32 - lo) * GP;
+        uint32_t word = 0;
+        if (p.per_head) {
+          const bool in = wi * 32 + lane < hi;
+          const float x = in ? at[lane * GP + warp].x : 0.f;
+          uint32_t open = __ballot_sync(0xffffffffu, in);
+          while (true) {
+            const uint32_t vote = __ballot_sync(0xffffffffu, !(x < w.bound)) & open;  // a NaN keeps
+            if (!vote) break;
+            const int src = 31 - __clz(vote);
+            word |= 1u << src;
+            open = (1u << src) - 1u;
+            w.take(at[src * GP + warp], thr);
+          }
+        } else {
+          const int g = lane & 7, j = lane >> 3;  // tiles wi * 32 + 31 - (4 i + j)
+          float x[8];
+          uint32_t open = 0;
 #pragma unroll
-      for (int g = 0; g < GMAX; ++g)
-        if (lane == g) {
-          sh.mfin[g] = m[g] == kNegInf ? 0.f : m[g];
-          sh.lfin[g] = l[g];
-          if (p.kept_tiles && rank == 0 && g < units) p.kept_tiles[gr.grp * units + g] = cnt[g];
+          for (int i = 0; i < 8; ++i) {
+            const int u = 31 - 4 * i - j;
+            const bool in = wi * 32 + u < hi && g < G;
+            x[i] = in ? at[u * GP + g].x : 0.f;
+            open |= (in ? 1u : 0u) << i;
+          }
+          while (true) {
+            uint32_t want = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) want |= (!(x[i] < w.bound) ? 1u : 0u) << i;  // a NaN keeps
+            want &= open;
+            const int first = __reduce_min_sync(0xffffffffu, want ? 4 * (__ffs(want) - 1) + j : 32);
+            if (first == 32) break;
+            word |= 0x80000000u >> first;
+            open &= 0xffu << (((first - j) >> 2) + 1);
+            if (g < G) w.take(at[(31 - first) * GP + g], thr);
+          }
         }
+        if (lane == 0) keep[(p.per_head ? warp : 0) * words + wi] = word;
+      }
     }
-    sm100::fence_proxy_async_smem();  // the ring's space goes back to the TMA
-    __syncthreads();
-  }
-
-  // ---- C: values of this block's kept tiles, a warp per chunk
-  float out[8][4];
-#pragma unroll
-  for (int db = 0; db < 8; ++db)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[db][i] = 0.f;
-  const float m0 = sh.mfin[2 * c], m1 = sh.mfin[2 * c + 1];
-  const int n_chunks = sh.items * 4;
-  phase = 0;
-  for (int x = warp; x < n_chunks && ok; x += NW) {
-    const uint32_t ent = list[x >> 2];
-    const int pos = (int)(ent & 0xffffffu) * T + (x & 3) * CK;
-    if (pos >= len) continue;
-    int a, b;
-    chunk_pages(pool, gr.b, pos, len, a, b, &sh.bad);
-    const uint32_t bar = smem_u32(&sh.pv[warp]);
+    hi = lo;
     __syncwarp();
-    if (lane == 0) {
-      mbar_expect_tx(bar, 2 * chunk_bytes(pool, a, b));
-      load_chunk(&tmK, pool, smem_u32(my), pos, gr.h, a, b, bar);
-      load_chunk(&tmV, pool, smem_u32(my + STAGE), pos, gr.h, a, b, bar);
-    }
-    float x0, x1, v0, v1;
-    fetch_scales(a, b, x0, x1);
-    v0 = a >= 0 ? pool.v_scale[(long long)a * pool.Hkv + gr.h] : 0.f;
-    v1 = b >= 0 ? pool.v_scale[(long long)b * pool.Hkv + gr.h] : v0;
-    ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort, 0x512));
-    phase ^= 1;
-    const bool has1 = pool.page == 16 ? b >= 0 : a >= 0;
-    float s[2][4];
-    chunk_scores(my, bq, pos, len, a >= 0, has1, undo0 * x0, undo1 * x0, undo0 * x1, undo1 * x1, s);
-    const bool on0 = (ent >> (24 + 2 * c)) & 1u, on1 = (2 * c + 1 < 8) && (ent >> (25 + 2 * c)) & 1u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float w[4];
-      w[0] = on0 ? ex2_approx(s[i][0] - m0 + kPShift) : 0.f;
-      w[1] = on1 ? ex2_approx(s[i][1] - m1 + kPShift) : 0.f;
-      w[2] = on0 ? ex2_approx(s[i][2] - m0 + kPShift) : 0.f;
-      w[3] = on1 ? ex2_approx(s[i][3] - m1 + kPShift) : 0.f;
-      if (i ? has1 : a >= 0) add_pv16(my + STAGE + i * 2048, len - pos - 16 * i, w, i ? v1 : v0, out);
-    }
+    if (hi > 0) __syncthreads();
   }
-  if (!ok) sm100::drain_in_flight();
+  if (p.per_head ? (warp < G && lane == 0) : tid < G) {
+    const int g = p.per_head ? warp : tid;
+    sh.mfin[g] = w.m == kNegInf ? 0.f : w.m;
+    sh.lfin[g] = w.l;
+  }
   __syncwarp();
-  const float one[2] = {1.f, 1.f};
-  join_and_store(p, sh, reinterpret_cast<float*>(ring), out, one, rank, o, false);
+  __syncthreads();
+  const int live = (nt + 31) / 32;
+  if (warp == 0) {  // the n-th kept tile (in the order of positions) is block n mod C's
+    int count = 0;
+    for (int w0 = 0; w0 < live; w0 += 32) {
+      uint32_t any = 0;
+      if (w0 + lane < live)
+        for (int u = 0; u < units; ++u) any |= keep[u * words + w0 + lane];
+      int at = __popc(any);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, at, 31);
+      at += count - __popc(any);
+      int mine = at / C, turn = at - mine * C;
+      while (any) {
+        const int bit = __ffs(any) - 1;
+        any &= any - 1;
+        if (turn == (int)rank) {
+          uint32_t heads = 0xffu;
+          if (p.per_head) {
+            heads = 0;
+            for (int u = 0; u < units; ++u) heads |= ((keep[u * words + w0 + lane] >> bit) & 1u) << u;
+          }
+          list[mine] = (uint32_t)((w0 + lane) * 32 + bit) | heads << 24;
+        }
+        if (++turn == C) {
+          turn = 0;
+          ++mine;
+        }
+      }
+      count += total;
+    }
+    if (lane == 0) sh.items = (count - (int)rank + C - 1) / C;
+  } else if (rank == 0) {
+    if (p.kept_tiles)
+      for (int u = warp - 1; u < units; u += NT / 32 - 1) {
+        int n = 0;
+        for (int e = lane; e < live; e += 32) n += __popc(keep[u * words + e]);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) p.kept_tiles[grp * units + u] = n;
+      }
+    if (p.keep_bits)
+      for (int e = tid - 32; e < units * p.nw; e += NT - 32) {
+        const int u = e / p.nw, wi = e - u * p.nw;
+        p.keep_bits[grp * units * p.nw + e] = wi < live ? keep[u * words + wi] : 0u;
+      }
+  }
+  sm100::fence_proxy_async_smem();  // the ring's space goes back to the TMA
+  __syncwarp();
+  __syncthreads();
 }
 
-__global__ void __launch_bounds__(NT, 1) dense_kernel(const __grid_constant__ CUtensorMap tmK,
-                                                      const __grid_constant__ CUtensorMap tmV,
-                                                      const Params p) {
-  extern __shared__ unsigned char raw[];
-  __shared__ Shared sh;
-  unsigned char* ring = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+// ------------------------------------------------------------------ the kernel
+template <int GH, bool RULE>
+__global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                       const __grid_constant__ CUtensorMap tmV,
+                                                       const Params p) {
+  constexpr int NCOL = TERMS * GH;
+  extern __shared__ unsigned char smem[];
+  Shared<GH>& sh = *reinterpret_cast<Shared<GH>*>(smem + RING);
+  if (smem_u32(smem) & 1023u) {  // the swizzle needs it; without static shared memory it holds
+    if (threadIdx.x == 0) record_layout_error(0x51f);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c = lane & 3;
   const int G = p.G, C = p.C;
   const Pool& pool = p.pool;
   const uint32_t rank = blockIdx.x;
-  const Group gr = group_of(p);
-  const int len = gr.len, nt = gr.nt;
-  __nv_bfloat16* o = p.o + gr.grp * G * D;
-  if (trivial(p, gr, rank, o)) return;
-  if (tid == 0) {
-    for (int w = 0; w < NW; ++w)
-      for (int s = 0; s < DENSE_NST; ++s) sm100::mbar_init(smem_u32(&sh.full[w][s]), 1);
-    sh.bad = sh.abort = 0;
-    sm100::fence_mbar_init();
+  const int h = blockIdx.y, b = blockIdx.z;
+  const long long grp = (long long)b * p.Hkv + h;
+  __nv_bfloat16* o = p.o + grp * G * D;
+
+  const int len = p.seq_lens[b];
+  uint4 qraw = make_uint4(0, 0, 0, 0);
+  if (tid < NC && (tid >> 4) < G)
+    qraw = *reinterpret_cast<const uint4*>(p.q + grp * G * D + tid * 8);
+  if (trivial(p, grp, len, rank, o)) return;
+  const int nt = (int)(((long long)len + T - 1) / T);
+  const int tiles = nt > (int)rank ? (nt - (int)rank + C - 1) / C : 0;  // this block's
+  const int units = p.per_head ? G : 1, words = rule_words(p.max_tiles);
+  float2* stats = reinterpret_cast<float2*>(smem + RING + sizeof(Shared<GH>));  // [slots][GP]
+  uint32_t* keep = reinterpret_cast<uint32_t*>(stats + (size_t)p.GP * rule_slots(p.max_tiles, C));
+  uint32_t* list = keep + units * words;
+  auto own_tile = [&](int i, int& pos, uint32_t& heads) {
+    pos = (i * C + (int)rank) * T;
+    heads = 0xffu;
+  };
+  bool ok = true;
+  if (warp == W_LOAD) {
+    if (lane == 0) {
+      for (int s = 0; s < NST; ++s) {
+        sm100::mbar_init(smem_u32(&sh.full[s]), 1);
+        sm100::mbar_init(smem_u32(&sh.empty[s]), 1);
+      }
+      for (int s = 0; s < 2; ++s) {
+        sm100::mbar_init(smem_u32(&sh.s_full[s]), 1);
+        sm100::mbar_init(smem_u32(&sh.o_full[s]), 1);
+        sm100::mbar_init(smem_u32(&sh.s_empty[s]), 4);
+        sm100::mbar_init(smem_u32(&sh.o_empty[s]), 4);
+        sm100::mbar_init(smem_u32(&sh.p_full[s]), 4);
+      }
+      sm100::fence_mbar_init();
+      sh.bad = sh.abort = 0;
+    }
+    __syncwarp();
+  } else if (warp == W_TMEM) {
+    sm100::tmem_alloc(smem_u32(&sh.tmem), 4 * NCOL);
+    sm100::tmem_relinquish();
+  } else if (warp < 4) {
+    split_q<GH>(qraw, sh, p.scale_log2);
+    sm100::fence_proxy_async_smem();
   }
-  const int units = p.per_head ? G : 1;
-  if (rank == 0) {  // every tile is kept
-    if (p.kept_tiles && tid < units) p.kept_tiles[gr.grp * units + tid] = nt;
+  sm100::tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  sm100::tc_fence_after();
+  float undo[GH], mref[GH], l[GH], out[GH];
+#pragma unroll
+  for (int g = 0; g < GH; ++g) {
+    undo[g] = sh.undo[g];
+    mref[g] = kNegInf;
+    l[g] = out[g] = 0.f;
+  }
+
+  if constexpr (RULE) {
+    // ---- A: statistics
+    if (warp == W_LOAD) {
+      ok = load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, false, 0u, 0u, own_tile);
+    } else if (warp == W_MMA) {
+      if (lane == 0)
+        for (int i = 0; i < tiles && ok; ++i) ok = issue_s<GH>(sh, smem, i, i);
+    } else if (warp < 4) {
+      for (int i = 0; i < tiles; ++i) {
+        float x[GH];
+        warp_wait(&sh.s_full[i & 1], (i >> 1) & 1, &sh.abort, 0x517);
+        scores<GH>(sh, i, sh.meta[i % NMETA], len, undo, x);
+        // a warp's 32 keys; a quarter without a finite score: mass 0
+        float m[GH];
+#pragma unroll
+        for (int g = 0; g < GH; ++g) {
+          m[g] = warp_max(x[g]);
+          x[g] = ex2_approx(x[g] - (m[g] == kNegInf ? 0.f : m[g]));
+        }
+        // sums: each step halves the heads a lane is at work on, lane / (32 / GH) is left with one
+#pragma unroll
+        for (int n = GH / 2, d = 16; n >= 1; n >>= 1, d >>= 1)
+#pragma unroll
+          for (int g = 0; g < n; ++g) {
+            const bool up = lane & d;
+            const float give = up ? x[g] : x[g + n], keep_ = up ? x[g + n] : x[g];
+            x[g] = keep_ + __shfl_xor_sync(0xffffffffu, give, d);
+            const float mk = up ? m[g + n] : m[g];
+            m[g] = mk;
+          }
+#pragma unroll
+        for (int d = 16 / GH; d >= 1; d >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
+        const int g = lane / (32 / GH);
+        if (lane % (32 / GH) == 0) sh.part[i & 1][warp][g] = make_float2(m[0], x[0]);
+        sync_softmax();
+        if (warp == (i & 3) && lane < G) {  // the four quarters' statistics as the tile's
+          float2 q[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) q[w] = sh.part[i & 1][w][lane];
+          float top = fmaxf(fmaxf(q[0].x, q[1].x), fmaxf(q[2].x, q[3].x));
+          const float z = top == kNegInf ? 0.f : top;
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) sum += q[w].y * ex2_approx(q[w].x - z);
+          if (isnan(sum)) top = sum;  // a tile with a NaN score is kept, and shows
+          stats[i * p.GP + lane] = make_float2(top, sum);
+        }
+      }
+    }
+    if (sh.abort) sm100::drain_in_flight();
+    __syncwarp();
+    if (C > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+
+    // ---- B
+    replay_rule<GH>(p, sh, smem, stats, keep, list, grp, len, nt, rank);
+
+    // ---- C: values of this block's kept tiles
+    const int items = sh.items;
+    const uint32_t done = (uint32_t)tiles;
+    if (warp == W_LOAD) {
+      auto kept_tile = [&](int i, int& pos, uint32_t& heads) {
+        const uint32_t x = list[i];
+        pos = (int)(x & 0xffffffu) * T;
+        heads = x >> 24;
+      };
+      if (ok) load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, items, true, done, done, kept_tile);
+    } else if (warp == W_MMA) {
+      if (lane == 0) {
+        for (int i = 0; i < 2 && i < items && ok; ++i) ok = issue_s<GH>(sh, smem, done + 2 * i, done + i);
+        for (int i = 0; i < items && ok; ++i) {
+          ok = issue_o<GH>(sh, smem, done + 2 * i + 1, i);
+          if (ok && i + 2 < items) ok = issue_s<GH>(sh, smem, done + 2 * (i + 2), done + i + 2);
+        }
+      }
+    } else if (warp < 4) {
+#pragma unroll
+      for (int g = 0; g < GH; ++g) mref[g] = g < G ? sh.mfin[g] : 0.f;
+      softmax_pv<GH, true>(sh, smem, len, items, done, done, undo, mref, l, out);
+    }
+  } else {
+    if (warp == W_LOAD) {
+      ok = load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, true, 0u, 0u, own_tile);
+    } else if (warp == W_MMA) {
+      if (lane == 0) {
+        for (int i = 0; i < 2 && i < tiles && ok; ++i) ok = issue_s<GH>(sh, smem, 2 * i, i);
+        for (int i = 0; i < tiles && ok; ++i) {
+          ok = issue_o<GH>(sh, smem, 2 * i + 1, i);
+          if (ok && i + 2 < tiles) ok = issue_s<GH>(sh, smem, 2 * (i + 2), i + 2);
+        }
+      }
+    } else if (warp < 4) {
+      softmax_pv<GH, false>(sh, smem, len, tiles, 0u, 0u, undo, mref, l, out);
+      // the block's mass per head: every thread has its own keys'
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], d);
+        if (lane == 0) sh.wm[warp][g] = l[g];
+      }
+      sync_softmax();
+      if (tid == 0)
+#pragma unroll
+        for (int g = 0; g < GH; ++g) {
+          sh.mfin[g] = mref[g];
+          sh.lfin[g] = (sh.wm[0][g] + sh.wm[1][g] + sh.wm[2][g] + sh.wm[3][g]) * (1.f / 256.f);
+        }
+    }
+  }
+  if (sh.abort) sm100::drain_in_flight();
+  sm100::tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  // given back here, by a warp whose lanes are together (behind the join's loops they need not
+  // be, and a deallocation by part of a warp never ends)
+  if (warp == W_TMEM) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc(sh.tmem, 4 * NCOL);
+  }
+  __syncwarp();
+  join_and_store<GH>(p, sh, *reinterpret_cast<Join*>(smem), out, rank, o, !RULE);
+  if (!RULE && rank == 0) {  // every tile is kept
+    if (p.kept_tiles && tid < units) p.kept_tiles[grp * units + tid] = nt;
     if (p.keep_bits)
       for (int e = tid; e < units * p.nw; e += NT) {
         const int left = nt - 32 * (e % p.nw);
-        p.keep_bits[gr.grp * units * p.nw + e] =
+        p.keep_bits[grp * units * p.nw + e] =
             left >= 32 ? 0xffffffffu : (left > 0 ? (1u << left) - 1u : 0u);
       }
   }
-  __syncthreads();
-  volatile int* abort = &sh.abort;
+}
 
-  uint32_t bq[8][2];
-  const float undo = load_q(p.q + gr.grp * G * D, G, bq) * p.scale_log2;
-  const float undo0 = __shfl_sync(0xffffffffu, undo, 8 * c);
-  const float undo1 = __shfl_sync(0xffffffffu, undo, 8 * c + 4);
-
-  unsigned char* my = ring + warp * (DENSE_NST * 2 * STAGE);
-  const int W = NW * C, wg = (int)rank * NW + warp;
-  const int all = (int)(((long long)len + CK - 1) / CK);
-  const int chunks = all > wg ? (all - wg + W - 1) / W : 0;
-  auto pos_of = [&](int k) { return (wg + k * W) * CK; };
-  int id0, id1, nid0 = -1, nid1 = -1;
-  float4 sc = make_float4(0.f, 0.f, 0.f, 0.f), nsc = sc;  // k, k (second page), v, v
-  auto fetch_ids = [&](int k, int& a, int& b) {
-    a = b = -1;
-    if (k < chunks) chunk_pages(pool, gr.b, pos_of(k), len, a, b, &sh.bad);
-  };
-  auto fetch_scales = [&](int a, int b, float4& x) {
-    x.x = a >= 0 ? pool.k_scale[(long long)a * pool.Hkv + gr.h] : 0.f;
-    x.z = a >= 0 ? pool.v_scale[(long long)a * pool.Hkv + gr.h] : 0.f;
-    x.y = b >= 0 ? pool.k_scale[(long long)b * pool.Hkv + gr.h] : x.x;
-    x.w = b >= 0 ? pool.v_scale[(long long)b * pool.Hkv + gr.h] : x.z;
-  };
-  auto issue = [&](int k, int a, int b) {
-    if (lane == 0) {
-      const int s = k % DENSE_NST;
-      const uint32_t bar = smem_u32(&sh.full[warp][s]), dst = smem_u32(my + s * 2 * STAGE);
-      mbar_expect_tx(bar, 2 * chunk_bytes(pool, a, b));
-      load_chunk(&tmK, pool, dst, pos_of(k), gr.h, a, b, bar);
-      load_chunk(&tmV, pool, dst + STAGE, pos_of(k), gr.h, a, b, bar);
-    }
-  };
-  fetch_ids(lane, id0, id1);
-#pragma unroll
-  for (int k = 0; k < DENSE_NST; ++k) {
-    const int a = __shfl_sync(0xffffffffu, id0, k), b = __shfl_sync(0xffffffffu, id1, k);
-    if (k < chunks) issue(k, a, b);
-  }
-  fetch_scales(id0, id1, sc);
-
-  float out[8][4];
-#pragma unroll
-  for (int db = 0; db < 8; ++db)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[db][i] = 0.f;
-  float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;  // l: this lane's keys only
-  bool ok = true;
-  int stage = 0;
-  uint32_t phase = 0;
-  for (int k = 0; k < chunks && ok; ++k) {
-    const int j = k & 31;
-    if (j == 0) {
-      if (k > 0) {
-        id0 = nid0;
-        id1 = nid1;
-        sc = nsc;
-      }
-      fetch_ids(k + 32 + lane, nid0, nid1);
-    } else if (j == 16) {
-      fetch_scales(nid0, nid1, nsc);
-    }
-    const int a = __shfl_sync(0xffffffffu, id0, j), b = __shfl_sync(0xffffffffu, id1, j);
-    const float x0 = __shfl_sync(0xffffffffu, sc.x, j), x1 = __shfl_sync(0xffffffffu, sc.y, j);
-    const float v0 = __shfl_sync(0xffffffffu, sc.z, j), v1 = __shfl_sync(0xffffffffu, sc.w, j);
-    const bool has1 = pool.page == 16 ? b >= 0 : a >= 0;
-    const int pos = pos_of(k);
-    ok = __all_sync(0xffffffffu,
-                    mbar_wait(smem_u32(&sh.full[warp][stage]), phase, abort, 0x513));
-    const unsigned char* st = my + stage * 2 * STAGE;
-    float s[2][4];
-    chunk_scores(st, bq, pos, len, a >= 0, has1, undo0 * x0, undo1 * x0, undo0 * x1, undo1 * x1, s);
-    float t0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
-    float t1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) {
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
-    }
-    if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
-      const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
-      const float f0 = m0 == kNegInf ? 0.f : ex2_approx(m0 - n0);
-      const float f1 = m1 == kNegInf ? 0.f : ex2_approx(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= f0;
-      l1 *= f1;
-#pragma unroll
-      for (int db = 0; db < 8; ++db) {
-        out[db][0] *= f0;
-        out[db][2] *= f0;
-        out[db][1] *= f1;
-        out[db][3] *= f1;
-      }
-    }
-    const float z0 = m0 == kNegInf ? 0.f : m0 - kPShift, z1 = m1 == kNegInf ? 0.f : m1 - kPShift;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float w[4];
-      w[0] = ex2_approx(s[i][0] - z0);
-      w[1] = ex2_approx(s[i][1] - z1);
-      w[2] = ex2_approx(s[i][2] - z0);
-      w[3] = ex2_approx(s[i][3] - z1);
-      l0 += w[0] + w[2];
-      l1 += w[1] + w[3];
-      if (i ? has1 : a >= 0) add_pv16(st + STAGE + i * 2048, len - pos - 16 * i, w, i ? v1 : v0, out);
-    }
-    const int nk = k + DENSE_NST, nj = nk & 31;
-    const bool next = (nk >> 5) != (k >> 5);
-    const int na = __shfl_sync(0xffffffffu, next ? nid0 : id0, nj);
-    const int nb = __shfl_sync(0xffffffffu, next ? nid1 : id1, nj);
-    __syncwarp();  // every lane has read the stages
-    if (nk < chunks && ok) issue(nk, na, nb);
-    if (++stage == DENSE_NST) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
-  if (!ok) sm100::drain_in_flight();
-#pragma unroll
-  for (int x = 4; x < 32; x <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-  }
-  if (lane < 4) {
-    sh.wm[warp][2 * c] = m0;
-    sh.wm[warp][2 * c + 1] = m1;
-    sh.wl[warp][2 * c] = l0;
-    sh.wl[warp][2 * c + 1] = l1;
-  }
-  __syncthreads();
-  float top0 = kNegInf, top1 = kNegInf;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    top0 = fmaxf(top0, sh.wm[w][2 * c]);
-    top1 = fmaxf(top1, sh.wm[w][2 * c + 1]);
-  }
-  if (tid < GMAX) {
-    float top = kNegInf, sum = 0.f;
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, sh.wm[w][tid]);
-    for (int w = 0; w < NW; ++w) {
-      const float x = sh.wm[w][tid];
-      sum += x == kNegInf ? sh.wl[w][tid] * 0.f : sh.wl[w][tid] * ex2_approx(x - top);
-    }
-    sh.mfin[tid] = top;
-    sh.lfin[tid] = sum * (1.f / 16384.f);
-  }
-  const float scale[2] = {m0 == kNegInf ? 0.f : ex2_approx(m0 - top0),
-                          m1 == kNegInf ? 0.f : ex2_approx(m1 - top1)};
-  join_and_store(p, sh, reinterpret_cast<float*>(ring), out, scale, rank, o, true);
+using Kernel = void (*)(CUtensorMap, CUtensorMap, Params);
+inline Kernel decode_kernel_of(int G, bool rule) {
+  if (G > 4) return rule ? decode_kernel<8, true> : decode_kernel<8, false>;
+  return rule ? decode_kernel<4, true> : decode_kernel<4, false>;
 }
 
 }  // namespace pdec

@@ -7,11 +7,17 @@ e4m3 2^-4):
       rounded: an error of at most (|x_i| + |x_j|) (2^-23 + 2 * 2^-24) =: (|x_i| + |x_j|) 2^-22.
   decode: a score is a float32 sum of 128 products, off by at most 128 * 2^-23 times the
       sum A of their magnitudes (a matrix instruction may cut where it does not round:
-      2^-23 a step), then scaled (three roundings) and, like the row's reference, taken
-      as a power of two: p is off by a relative 2 (128 * 2^-23 + 4 * 2^-24) A + 2^-21. P is rounded
-      to f16 for the product with V: 2^-11. The sum l has the same error as p. Then the
-      output's rounding to bf16. With S = sum p |v|:
-      |o - ref| <= 2^-8 |ref| + S (2^-11 + 4 (129 * 2^-23) A + 2^-20).
+      2^-23 a step). q goes in as the sum of four e4m3 terms, each the rounded rest of the
+      ones before, 2^4 apart: what is left after the last is half its smallest step, 2^-10 / 2^12
+      with the largest value scaled to at least 2^7: 2^-29 max|q| an element. Then the score is scaled
+      (three roundings) and, like the row's reference, taken as a power of two: p is off by
+      a relative 2 ((128 * 2^-23 + 4 * 2^-24) A + 2^-29 max|q| sum|k|) + 2^-21. P is rounded
+      to f16 for the product with V: 2^-11. It goes in as three e4m3 terms in the same
+      way, scaled to at most 2^8 with the largest p of its 32 keys at 2^8: what is left is at most 2^-10 /
+      2^8 / 2^8 = 2^-26 of that largest p. The sum l has the same error as p. Then the
+      output's rounding to bf16. With S = sum p |v|, U = sum over 32-key chunks of (largest p
+      of the chunk) * (sum |v| of the chunk):
+      |o - ref| <= 2^-8 |ref| + S (2^-11 + 4 (129 * 2^-23 A + 2^-29 max|q| sum|k|) + 2^-20) + 2^-26 U.
 """
 
 from __future__ import annotations
@@ -176,9 +182,14 @@ def sequence(cache_tensors, table, b, n):
 
 def decode_bound(q, K, V, ref, keep_keys):
     """|o - ref| bound of one query head: q [128], K, V [n, 128], keep_keys [n] bool."""
-    A = (np.abs(K[keep_keys]) @ np.abs(q)).max() / math.sqrt(D)
-    s = (K[keep_keys] @ q) / math.sqrt(D)
+    k = K[keep_keys]
+    A = (np.abs(k) @ np.abs(q)).max() / math.sqrt(D)
+    B = 2.0 ** -29 * np.abs(q).max() * np.abs(k).sum(-1).max() / math.sqrt(D)
+    s = np.where(keep_keys, (K @ q) / math.sqrt(D), -np.inf)
     p = np.exp(s - s.max())
     p /= p.sum()
-    S = p @ np.abs(V[keep_keys])
-    return 2.0 ** -8 * np.abs(ref) + S * (2.0 ** -11 + 4 * 129 * 2.0 ** -23 * A + 2.0 ** -20)
+    S = p @ np.abs(V)
+    edges = np.arange(0, len(p), 32)
+    U = np.maximum.reduceat(p, edges) @ np.add.reduceat(np.abs(V), edges, axis=0)
+    return 2.0 ** -8 * np.abs(ref) + S * (2.0 ** -11 + 4 * (129 * 2.0 ** -23 * A + B) + 2.0 ** -20) \
+        + 2.0 ** -26 * U
