@@ -2,8 +2,6 @@
 // checks and launches (the contract is in include/mala.h).
 #pragma once
 
-#include <atomic>
-
 #include "api.cuh"
 #include "decode_paged_sm100.cuh"
 #include "paged.cuh"
@@ -75,50 +73,16 @@ inline bool make_page_map(CUtensorMap* m, const void* base, const paged::Pool& p
   return r == CUDA_SUCCESS;
 }
 
-// Clusters of C blocks of a decode kernel that the device holds at once, with one or two
-// blocks to an SM. What the driver says is kept: the question takes microseconds.
-inline int resident_clusters(bool wide, bool rule, int C, size_t smem) {
-  static std::atomic<int> known[2][2][2][pdec::MAXC + 1];  // 0: not asked yet
-  std::atomic<int>& k = known[wide][rule][smem <= 113 * 1024][C];
-  int n = k.load(std::memory_order_relaxed);
-  if (n > 0) return n - 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C, 1, 1);
-  cfg.blockDim = dim3(pdec::NT, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, pdec::decode_kernel_of(wide ? pdec::GMAX : 1, rule),
-                                     &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
-  k.store(n + 1, std::memory_order_relaxed);
-  return n;
-}
-
 // Blocks of a decode cluster, 0 when the statistics of the longest sequence do not fit.
 inline int decode_cluster(const pdec::Params& p, long long groups, bool rule, size_t* smem) {
   int best = 0;
-  double least = 0;
-  for (int C = 1; C <= pdec::MAXC; ++C) {
-    if (best > 0 && C > p.max_tiles) break;
+  for (int C = 1; C <= pdec::MAXC; C *= 2) {
     const size_t need = pdec::smem_bytes(p.G, p.max_tiles, C, p.per_head, rule);
     if (need > pdec::MAX_SMEM) continue;
-    const int resident = resident_clusters(p.G > 4, rule, C, need);
-    if (resident < 1) continue;
-    const double waves = (double)((groups + resident - 1) / resident);
-    const double cost = waves * ((double)((p.max_tiles + C - 1) / C) + 8.0);
-    if (best == 0 || cost < least) {
-      best = C;
-      least = cost;
-      *smem = need;
-    }
+    const long long slots = (long long)sm_count() * (need <= 113 * 1024 ? 2 : 1);
+    if (best > 0 && (10 * groups * C > 13 * slots || C / 2 >= p.max_tiles)) break;
+    best = C;
+    *smem = need;
   }
   return best;
 }
@@ -234,9 +198,13 @@ mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q, void
   MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)mala::pdec::MAX_SMEM));
   MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  // without this an SM takes one block, although the shared memory of two fits
+  MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared));
   size_t smem;
   p.C = decode_cluster(p, (long long)batch * Hkv, rule, &smem);
   if (p.C < 1) return MALA_ERR_TOO_LARGE;
+  while (1 << p.C_log2 < p.C) ++p.C_log2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.C, Hkv, batch);
   cfg.blockDim = dim3(mala::pdec::NT, 1, 1);

@@ -52,6 +52,7 @@ constexpr int GMAX = 8;
 constexpr int NT = 256;               // warps 0 - 3 softmax, 4 loads, 5 products, 6 holds the tensor
                                       // memory, 6 and 7 help in B
 constexpr int NC = 128;               // softmax threads
+static_assert(NT - 32 == 224, "the number in the second named barrier");
 constexpr int W_LOAD = 4, W_MMA = 5, W_TMEM = 6;
 constexpr uint32_t TILE_BYTES = T * D;
 constexpr int NST = 5;                // ring stages (tiles)
@@ -65,7 +66,7 @@ struct Params {
   const __nv_bfloat16* q;  // [batch][Hq][128]
   __nv_bfloat16* o;
   const int32_t* seq_lens;
-  int G, GP, Hkv, max_len, max_tiles, C;  // GP: G rounded up to even
+  int G, GP, Hkv, max_len, max_tiles, C, C_log2;  // GP: G rounded up to even; C a power of two
   float scale_log2, log2_tau;
   int per_head;
   int32_t* kept_tiles;
@@ -166,6 +167,13 @@ struct alignas(16) Meta {
   float k[8], v[8];
 };
 
+// What the cluster's blocks send each other at the end.
+struct Join {
+  float recv[GMAX * (D + MAXC)];  // partial outputs of this block's dimensions, by sender
+  float2 ml[MAXC][GMAX];
+  int bad[MAXC];
+};
+
 template <int GH>
 struct Shared {
   unsigned char p[2][T * TERMS * GH];  // P of a tile: key k's terms in rows of sixteen bytes
@@ -176,16 +184,11 @@ struct Shared {
   uint64_t s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2];
   float undo[GMAX];                    // what a head's products are multiplied with
   float mfin[GMAX], lfin[GMAX];        // final max (log2 units) and mass
+  float bound[GMAX];
   float wm[4][GMAX];
   int bad, abort, items;
   uint32_t tmem;
-};
-
-// The end of the kernel, in the ring's space: what the cluster's blocks send each other.
-struct Join {
-  float recv[GMAX * (D + MAXC)];  // partial outputs of this block's dimensions, by sender
-  float2 ml[MAXC][GMAX];
-  int bad[MAXC];
+  alignas(16) Join join;
 };
 
 // Shared memory behind the ring and Shared: statistics [slots][GP] of tiles t = slot C + rank, the
@@ -297,8 +300,10 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
     if (i < tiles) {
       place(i, pos, heads);
       const int at = pos + sub * pool.page, slot = at >> pool.page_log2;
-      if (at < len) {
-        if (slot < pool.max_pages) id = row[slot];
+      if (slot < pool.max_pages) id = row[slot];  // whether it is needed or not: len is on its way
+      if (at >= len) {
+        id = -1;
+      } else {
         if ((unsigned)id >= (unsigned)pool.num_pages) {
           record_bad_page(0x500);
           sh.bad = 1;
@@ -523,10 +528,11 @@ __device__ __forceinline__ void softmax_pv(Shared<GH>& sh, unsigned char* ring, 
 // sh.lfin is the whole cluster's mass. Each block owns some of the dimensions, and the others
 // write their partial sums of them into its shared memory: no round trips.
 template <int GH>
-__device__ __forceinline__ void join_and_store(const Params& p, Shared<GH>& sh, Join& jn,
+__device__ __forceinline__ void join_and_store(const Params& p, Shared<GH>& sh,
                                                const float (&out)[GH], uint32_t rank,
                                                __nv_bfloat16* o, bool dense) {
   const int tid = threadIdx.x, C = p.C, G = p.G;
+  Join& jn = sh.join;
   const float nan = __int_as_float(0x7fc00000);
   if (C == 1) {
     if (tid < NC)
@@ -535,8 +541,6 @@ __device__ __forceinline__ void join_and_store(const Params& p, Shared<GH>& sh, 
         if (g < G) o[g * D + tid] = __float2bfloat16_rn(sh.bad ? nan : out[g] / sh.lfin[g]);
     return;
   }
-  cluster_arrive();  // the ring is free, and may be written to by the other blocks
-  cluster_wait();
   const int each = (D + C - 1) / C;  // dimensions a block owns
   if (tid < NC) {
     const int owner = tid / each, i = tid - owner * each;
@@ -597,19 +601,24 @@ __device__ __forceinline__ bool trivial(const Params& p, long long grp, int len,
 struct Walk {
   float m, l, bound;
   __device__ __forceinline__ void take(float2 s, float thr) {
-    const float mn = fmaxf(m, s.x);
-    const float z = mn == kNegInf ? 0.f : mn;
-    l = l * ex2_approx(m - z) + s.y * ex2_approx(s.x - z);
-    m = mn;
-    bound = mn + lg2_approx(l) + thr;
+    const float d = s.x - m;
+    const bool up = !(d <= 0.f);  // a NaN, too
+    const float f = ex2_approx(m == kNegInf ? kNegInf : -fabsf(d));  // the smaller one's share
+    l = up ? fmaf(l, f, s.y) : fmaf(s.y, f, l);
+    m = up ? s.x : m;
+    bound = m + lg2_approx(l) + thr;
   }
 };
 
 // Phase B: replays the rule over the cluster's statistics, newest first, in stretches that
 // fit in the ring's space (a single block's statistics lie in tile order already); leaves the
-// rows' final max and mass, the keep bits, and this block's list of tiles. Group: one warp,
-// lane = (head, tile mod 4), 32 tiles at a time in registers; a kept tile costs one look-up
-// and one update, all heads at once. Per head: a warp per head, lane = tile.
+// rows' final max and mass, the keep bits, and this block's list of tiles.
+//
+// A head's bound never falls, so a tile below the bound as it stands now is out for good:
+// the warps sort out, side by side, those that no head could still want at the bound that the
+// newest 32 tiles left, and only the others are looked at one by one (vote and update, about 150
+// cycles each). Group: one warp, a lane per head. Per head: a warp
+// per head.
 template <int GH>
 __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, unsigned char* smem,
                                             float2* stats, uint32_t* keep, uint32_t* list,
@@ -621,6 +630,10 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
   const int cap = C > 1 ? ((int)(RING / sizeof(float2)) / GP) & ~31 : 0x7fffffe0;
   const uint32_t stats_a = smem_u32(stats);
   const float thr = p.log2_tau - lg2_approx((float)len);
+  const int unit = p.per_head ? warp : 0;  // whose tiles this warp walks
+  const bool walks = p.per_head ? warp < G : warp == 0;
+  const int head = p.per_head ? warp : lane & 7;
+  const int seen = head < G ? head : G - 1;  // lanes without a head follow one that is there
   Walk w = {kNegInf, 0.f, kNegInf};
   for (int hi = nt; hi > 0;) {
     const int lo = hi > cap ? (hi - cap + 31) & ~31 : 0;
@@ -632,9 +645,9 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
         for (int u = 0; u < 4; ++u) {
           const int e = e0 + u * NT;
           if (e >= n) break;
-          const int t = lo + e / per, slot = t / C;
+          const int t = lo + e / per, slot = t >> p.C_log2;
           x[u] = sm100::ld_cluster_f32x4(sm100::mapa_rank(
-              stats_a + 16u * (uint32_t)(slot * per + e % per), (uint32_t)(t - slot * C)));
+              stats_a + 16u * (uint32_t)(slot * per + e % per), (uint32_t)(t & (C - 1))));
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -645,48 +658,82 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
       __syncwarp();
       __syncthreads();
     }
-    if (p.per_head ? warp < G : warp == 0) {
-      for (int wi = (hi - 1) >> 5; wi >= lo >> 5; --wi) {
-        const float2* at = loc + (size_t)(wi * 32 - lo) * GP;
-        uint32_t word = 0;
-        if (p.per_head) {
-          const bool in = wi * 32 + lane < hi;
-          const float x = in ? at[lane * GP + warp].x : 0.f;
-          uint32_t open = __ballot_sync(0xffffffffu, in);
-          while (true) {
-            const uint32_t vote = __ballot_sync(0xffffffffu, !(x < w.bound)) & open;  // a NaN keeps
-            if (!vote) break;
-            const int src = 31 - __clz(vote);
-            word |= 1u << src;
-            open = (1u << src) - 1u;
-            w.take(at[src * GP + warp], thr);
-          }
-        } else {
-          const int g = lane & 7, j = lane >> 3;  // tiles wi * 32 + 31 - (4 i + j)
-          float x[8];
-          uint32_t open = 0;
+    const int last = (hi - 1) >> 5, first = lo >> 5;
+    // the tiles of word wi that are `open`, newest first; the word comes out as what is kept.
+    // `all`: take the newest of them whatever it is, and sort the rest out at its bound.
+    auto walk = [&](int wi, uint32_t open, bool all) {
+      const float2* at = loc + (size_t)(wi * 32 - lo) * GP;
+      uint32_t word = 0;
+      if (all) {
+        const int bit = 31 - __clz(open);
+        word = 1u << bit;
+        w.take(at[bit * GP + seen], thr);
+        if (!p.per_head) {
+          if (lane < G) sh.bound[lane] = w.bound;
+          __syncwarp();
+        }
+        bool may = false;
+        if (lane < bit) {
+          if (p.per_head) {
+            may = !(at[lane * GP + head].x < w.bound);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int u = 31 - 4 * i - j;
-            const bool in = wi * 32 + u < hi && g < G;
-            x[i] = in ? at[u * GP + g].x : 0.f;
-            open |= (in ? 1u : 0u) << i;
-          }
-          while (true) {
-            uint32_t want = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) want |= (!(x[i] < w.bound) ? 1u : 0u) << i;  // a NaN keeps
-            want &= open;
-            const int first = __reduce_min_sync(0xffffffffu, want ? 4 * (__ffs(want) - 1) + j : 32);
-            if (first == 32) break;
-            word |= 0x80000000u >> first;
-            open &= 0xffu << (((first - j) >> 2) + 1);
-            if (g < G) w.take(at[(31 - first) * GP + g], thr);
+            for (int g = 0; g < GH; ++g)
+              if (g < G) may |= !(at[lane * GP + g].x < sh.bound[g]);
           }
         }
-        if (lane == 0) keep[(p.per_head ? warp : 0) * words + wi] = word;
+        open = __ballot_sync(0xffffffffu, may);
       }
+      int bit = 31 - __clz(open | 1u);
+      float2 x = at[bit * GP + seen];
+      while (open) {
+        open &= ~(1u << bit);
+        const int next = 31 - __clz(open | 1u);
+        const float2 y = at[next * GP + seen];  // on its way while this one is decided
+        if (__any_sync(0xffffffffu, !(x.x < w.bound))) {  // a NaN keeps
+          word |= 1u << bit;
+          w.take(x, thr);
+        }
+        bit = next;
+        x = y;
+      }
+      if (lane == 0) keep[unit * words + wi] = word;
+    };
+    if (walks) {
+      const int in = hi - last * 32;
+      walk(last, in >= 32 ? 0xffffffffu : (1u << in) - 1u, hi == nt);
+      if (p.per_head ? lane == 0 : lane < G) sh.bound[p.per_head ? warp : lane] = w.bound;
     }
+    __syncwarp();
+    __syncthreads();
+    for (int wi = first + warp; wi < last; wi += NT / 32) {
+      const float2* at = loc + (size_t)(wi * 32 + lane - lo) * GP;
+      bool may = false;
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+        if (g >= G) break;
+        const bool wants = !(at[g].x < sh.bound[g]);
+        may |= wants;
+        if (p.per_head) {
+          const uint32_t open = __ballot_sync(0xffffffffu, wants);
+          if (lane == 0) keep[g * words + wi] = open;
+        }
+      }
+      const uint32_t open = __ballot_sync(0xffffffffu, may);
+      if (!p.per_head && lane == 0) keep[wi] = open;
+    }
+    __syncwarp();
+    __syncthreads();
+    if (walks)
+      for (int w0 = last - 1; w0 >= first; w0 -= 32) {  // 32 words at a time, a lane each
+        const uint32_t mine = w0 - lane >= first ? keep[unit * words + w0 - lane] : 0u;
+        uint32_t some = __ballot_sync(0xffffffffu, mine != 0u);
+        while (some) {
+          const int src = __ffs(some) - 1;
+          some &= some - 1;
+          walk(w0 - src, __shfl_sync(0xffffffffu, mine, src), false);
+        }
+      }
     hi = lo;
     __syncwarp();
     if (hi > 0) __syncthreads();
@@ -713,7 +760,7 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
       }
       const int total = __shfl_sync(0xffffffffu, at, 31);
       at += count - __popc(any);
-      int mine = at / C, turn = at - mine * C;
+      int mine = at >> p.C_log2, turn = at & (C - 1);
       while (any) {
         const int bit = __ffs(any) - 1;
         any &= any - 1;
@@ -732,7 +779,7 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
       }
       count += total;
     }
-    if (lane == 0) sh.items = (count - (int)rank + C - 1) / C;
+    if (lane == 0) sh.items = (count - (int)rank + C - 1) >> p.C_log2;
   } else if (rank == 0) {
     if (p.kept_tiles)
       for (int u = warp - 1; u < units; u += NT / 32 - 1) {
@@ -776,18 +823,6 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
   uint4 qraw = make_uint4(0, 0, 0, 0);
   if (tid < NC && (tid >> 4) < G)
     qraw = *reinterpret_cast<const uint4*>(p.q + grp * G * D + tid * 8);
-  if (trivial(p, grp, len, rank, o)) return;
-  const int nt = (int)(((long long)len + T - 1) / T);
-  const int tiles = nt > (int)rank ? (nt - (int)rank + C - 1) / C : 0;  // this block's
-  const int units = p.per_head ? G : 1, words = rule_words(p.max_tiles);
-  float2* stats = reinterpret_cast<float2*>(smem + RING + sizeof(Shared<GH>));  // [slots][GP]
-  uint32_t* keep = reinterpret_cast<uint32_t*>(stats + (size_t)p.GP * rule_slots(p.max_tiles, C));
-  uint32_t* list = keep + units * words;
-  auto own_tile = [&](int i, int& pos, uint32_t& heads) {
-    pos = (i * C + (int)rank) * T;
-    heads = 0xffu;
-  };
-  bool ok = true;
   if (warp == W_LOAD) {
     if (lane == 0) {
       for (int s = 0; s < NST; ++s) {
@@ -805,23 +840,44 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
       sh.bad = sh.abort = 0;
     }
     __syncwarp();
-  } else if (warp == W_TMEM) {
-    sm100::tmem_alloc(smem_u32(&sh.tmem), 4 * NCOL);
-    sm100::tmem_relinquish();
-  } else if (warp < 4) {
-    split_q<GH>(qraw, sh, p.scale_log2);
-    sm100::fence_proxy_async_smem();
   }
-  sm100::tc_fence_before();
-  __syncwarp();
   __syncthreads();
-  sm100::tc_fence_after();
+  if (trivial(p, grp, len, rank, o)) return;
+  if (!RULE && C > 1) cluster_arrive();
+  const int nt = (int)(((long long)len + T - 1) / T);
+  const int tiles = nt > (int)rank ? (nt - (int)rank + C - 1) / C : 0;  // this block's
+  const int units = p.per_head ? G : 1, words = rule_words(p.max_tiles);
+  float2* stats = reinterpret_cast<float2*>(smem + RING + sizeof(Shared<GH>));  // [slots][GP]
+  uint32_t* keep = reinterpret_cast<uint32_t*>(stats + (size_t)p.GP * rule_slots(p.max_tiles, C));
+  uint32_t* list = keep + units * words;
+  __syncwarp();  // here and below: a warp-wide instruction or barrier wants its lanes together
+
+  auto own_tile = [&](int i, int& pos, uint32_t& heads) {
+    pos = (i * C + (int)rank) * T;
+    heads = 0xffu;
+  };
+  bool ok = true;
   float undo[GH], mref[GH], l[GH], out[GH];
 #pragma unroll
   for (int g = 0; g < GH; ++g) {
-    undo[g] = sh.undo[g];
+    undo[g] = 0.f;
     mref[g] = kNegInf;
     l[g] = out[g] = 0.f;
+  }
+  if (warp != W_LOAD) {  // the load warp needs none of this
+    if (warp == W_TMEM) {
+      sm100::tmem_alloc(smem_u32(&sh.tmem), 4 * NCOL);
+      sm100::tmem_relinquish();
+    } else if (warp < 4) {
+      split_q<GH>(qraw, sh, p.scale_log2);
+      sm100::fence_proxy_async_smem();
+    }
+    sm100::tc_fence_before();
+    __syncwarp();
+    asm volatile("barrier.cta.sync 2, 224;" ::: "memory");
+    sm100::tc_fence_after();
+#pragma unroll
+    for (int g = 0; g < GH; ++g) undo[g] = sh.undo[g];
   }
 
   if constexpr (RULE) {
@@ -947,8 +1003,8 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     sm100::tc_fence_after();
     sm100::tmem_dealloc(sh.tmem, 4 * NCOL);
   }
-  __syncwarp();
-  join_and_store<GH>(p, sh, *reinterpret_cast<Join*>(smem), out, rank, o, !RULE);
+  if (!RULE && C > 1) cluster_wait();  // the other blocks run
+  join_and_store<GH>(p, sh, out, rank, o, !RULE);
   if (!RULE && rank == 0) {  // every tile is kept
     if (p.kept_tiles && tid < units) p.kept_tiles[grp * units + tid] = nt;
     if (p.keep_bits)
