@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 __all__ = ["mala_fwd", "mala_fwd_varlen", "mala_bwd", "mala_decode", "mala_decode_noalloc", "mala_check",
            "PagedCache", "mala_cache_append", "mala_decode_paged", "mala_cache_gather",
@@ -474,7 +475,7 @@ class PagedCache:
         n, Hkv, page, d = k_pages.shape
         self._tensors = (k_pages, v_pages, k_scale, v_scale, page_table)
         self._device = k_pages.device
-        self._index = self._device.index
+        self._index = k_pages.get_device()
         self.Hkv, self.page_size = Hkv, page
         self.sequences, max_pages = page_table.shape
         self.max_seqlen = max_pages * page
@@ -494,32 +495,38 @@ class PagedCache:
 
 
 def _paged_ready(cache, require_cuda=True):
+    """The checks that come first; returns torch. (A decode step's host time counts: the
+    functions below look each attribute of a tensor up once.)"""
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
+    torch = sys.modules["torch"]  # imported, since there is a cache
     if require_cuda:
-        if cache._device.type != "cuda":
+        if cache._index < 0:
             raise ValueError("the cache must be on a CUDA device")
-        if cache._index != _torch().cuda.current_device():
+        if cache._index != torch._C._cuda_getDevice():
             raise ValueError(f"the cache is on {cache._device}, not on the current CUDA device "
                              "(torch.cuda.set_device)")
+    return torch
 
 
 def _paged_stream(stream, index):
     """The stream's handle as a plain number (the current stream of device ``index`` when
-    None), without building a stream object: a decode step's host time counts."""
+    None), without building a stream object."""
     if stream is not None:
         return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(index)
+    return sys.modules["torch"]._C._cuda_getCurrentRawStream(index)
 
 
-def _check_lens(cache, t, name, n=None):
-    torch = _torch()
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+def _check_lens(torch, cache, t, name, n=None):
+    """A contiguous 1-D int32 tensor of n entries: (pointer, entries)."""
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
-    if t.device != cache._device:
+    if t.get_device() != cache._index:
         raise ValueError(f"{name} must be on {cache._device}")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} must hold {n} entries, got {t.shape[0]}")
+    if n is not None and shape[0] != n:
+        raise ValueError(f"{name} must hold {n} entries, got {shape[0]}")
+    return t.data_ptr(), shape[0]
 
 
 def _check_batch(cache, batch):
@@ -528,25 +535,27 @@ def _check_batch(cache, batch):
                          f"{cache.sequences} rows")
 
 
-def _rows(cache, t, name, total, heads):
-    """bf16 [total, heads, 128] with rows that may lie apart: (pointer, token stride,
-    head stride)."""
-    torch = _torch()
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.device != cache._device:
+def _rows(torch, cache, t, name, total, heads):
+    """bf16 [total, heads, 128] with rows that may lie apart (None: any number of them):
+    (pointer, token stride, head stride, total, heads)."""
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or t.get_device() != cache._index \
+            or (cache._index < 0 and t.device != cache._device):
         raise ValueError(f"{name} must be a bf16 [tokens, heads, d] tensor on {cache._device}")
-    if t.shape[0] != total or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must have shape ({total}, {heads or 'heads'}, 128), got "
-                         f"{tuple(t.shape)}")
+    n, h, d = shape
+    if (total is not None and n != total) or d != 128 or (heads is not None and h != heads):
+        raise ValueError(f"{name} must have shape ({total or 'tokens'}, {heads or 'heads'}, 128), "
+                         f"got {tuple(shape)}")
     ts, hs, ds = t.stride()
-    if t.shape[0] == 1:
+    if n == 1:
         ts = 0
-    if t.shape[1] == 1:
+    if h == 1:
         hs = 0
     ptr = t.data_ptr()
-    if total and (ds != 1 or ts % 8 or hs % 8 or ptr % 16):
+    if n and (ds != 1 or ts % 8 or hs % 8 or ptr % 16):
         raise ValueError(f"{name}: d must be contiguous, the strides multiples of 8 elements and "
                          "the start 16-byte aligned")
-    return ptr, ts, hs
+    return ptr, ts, hs, n, h
 
 
 def mala_cache_append(cache, k, v, seq_lens, cu_seqlens=None, max_new: int | None = None,
@@ -562,53 +571,53 @@ def mala_cache_append(cache, k, v, seq_lens, cu_seqlens=None, max_new: int | Non
     [rot_dim / 2], rot_dim a multiple of 16 (None: no rotation); interleaved: pairs (2i, 2i+1)
     instead of (i, i + rot_dim / 2). Returns q rotated (q_out, which may be q; a new
     tensor if None), or None without q."""
-    torch = _torch()
-    _paged_ready(cache)
-    total = k.shape[0]
-    _check_lens(cache, seq_lens, "seq_lens")
-    batch = seq_lens.shape[0]
+    torch = _paged_ready(cache)
+    lens, batch = _check_lens(torch, cache, seq_lens, "seq_lens")
     _check_batch(cache, batch)
+    kp, kt, kh, total, _ = _rows(torch, cache, k, "k", None, cache.Hkv)
+    cu = None
     if cu_seqlens is None:
         if total != batch:
             raise ValueError("without cu_seqlens every sequence has one new token")
         max_new = 1
     else:
-        _check_lens(cache, cu_seqlens, "cu_seqlens", batch + 1)
+        cu, _ = _check_lens(torch, cache, cu_seqlens, "cu_seqlens", batch + 1)
         max_new = total if max_new is None else int(max_new)
         if max_new < 0:
             raise ValueError("max_new must not be negative")
-    kr = _rows(cache, k, "k", total, cache.Hkv)
-    vr = _rows(cache, v, "v", total, cache.Hkv)
-    qr = qo = (None, 0, 0)
-    Hq = 0
+    vp, vt, vh, _, _ = _rows(torch, cache, v, "v", total, cache.Hkv)
+    qp = op = None
+    qt = qh = ot = oh = Hq = 0
     if q is not None:
-        qr = _rows(cache, q, "q", total, None)
-        Hq = q.shape[1]
+        qp, qt, qh, _, Hq = _rows(torch, cache, q, "q", total, None)
         if Hq < 1 or Hq % cache.Hkv:
             raise ValueError("the query heads must be a multiple of the key/value heads")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qo = _rows(cache, q_out, "q_out", total, Hq)
-        if qo[0] == qr[0] and qo != qr:
-            raise ValueError("q_out may be q itself, or must not overlap it")
-        if total > 1 and qo[1] == 0 or Hq > 1 and qo[2] == 0:
-            raise ValueError("q_out's rows must not overlap")
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            op, ot, oh = q_out.data_ptr(), Hq * 128, 128
+        else:
+            op, ot, oh, _, _ = _rows(torch, cache, q_out, "q_out", total, Hq)
+            if op == qp and (ot != qt or oh != qh):
+                raise ValueError("q_out may be q itself, or must not overlap it")
+            if total > 1 and ot == 0 or Hq > 1 and oh == 0:
+                raise ValueError("q_out's rows must not overlap")
     elif q_out is not None:
         raise ValueError("q_out without q")
     rot, freq = 0, None
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() \
-                or inv_freq.device != cache._device:
+        shape = inv_freq.shape
+        if inv_freq.dtype is not torch.float32 or len(shape) != 1 \
+                or not inv_freq.is_contiguous() or inv_freq.get_device() != cache._index:
             raise ValueError(f"inv_freq must be a contiguous 1-D float32 tensor on {cache._device}")
-        rot = 2 * inv_freq.shape[0]
+        rot = 2 * shape[0]
         if rot % 16 or rot > 128:
             raise ValueError("rot_dim = 2 * len(inv_freq) must be a multiple of 16, at most d")
         freq = inv_freq.data_ptr() if rot else None
-    code = lib().mala_cache_append(cache._ref, *kr, *vr, *qr, *qo,
-                                   None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                                   seq_lens.data_ptr(), batch, total, max_new, Hq, freq, rot,
-                                   int(bool(interleaved)), _paged_stream(stream, cache._index))
-    _raise(code, "mala_cache_append")
+    code = lib().mala_cache_append(cache._ref, kp, kt, kh, vp, vt, vh, qp, qt, qh, op, ot, oh, cu,
+                                   lens, batch, total, max_new, Hq, freq, rot,
+                                   1 if interleaved else 0, _paged_stream(stream, cache._index))
+    if code:
+        _raise(code, "mala_cache_append")
     return q_out
 
 
@@ -621,30 +630,31 @@ def mala_decode_paged(q, cache, seq_lens, tau: float = 1.0, scale: float = 0.0,
     what the page table can hold). Returns o like q or, with ``trace=True``, (o, kept_tiles
     [batch, Hkv], keep_bits [batch, Hkv, nw]), per query head with ``per_head=True``;
     nw covers max_seqlen."""
-    torch = _torch()
-    _paged_ready(cache)
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous() \
-            or q.device != cache._device:
+    torch = _paged_ready(cache)
+    shape = q.shape
+    if q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != 128 \
+            or not q.is_contiguous() or q.get_device() != cache._index:
         raise ValueError(f"q must be a contiguous bf16 [batch, Hq, 128] tensor on {cache._device}")
-    batch, Hq, _ = q.shape
+    batch, Hq, _ = shape
     _check_batch(cache, batch)
     if Hq < 1 or Hq % cache.Hkv:
         raise ValueError("the query heads must be a multiple of the key/value heads")
-    _check_lens(cache, seq_lens, "seq_lens", batch)
+    lens, _ = _check_lens(torch, cache, seq_lens, "seq_lens", batch)
     limit = cache.max_seqlen if max_seqlen is None else int(max_seqlen)
     if limit < 1:
         raise ValueError("max_seqlen must be positive")
-    o = torch.empty_like(q) if out is None else _buf(out, "out", cache._device, q.dtype, q.shape)
+    o = torch.empty_like(q) if out is None else _buf(out, "out", cache._device, q.dtype, shape)
     kept = bits = None
     if trace:
         rows = Hq if per_head else cache.Hkv
         kept = torch.empty((batch, rows), dtype=torch.int32, device=q.device)
         bits = torch.empty((batch, rows, (n_blocks(limit, 128) + 31) // 32), dtype=torch.int32,
                            device=q.device)
-    code = lib().mala_decode_paged(cache._ref, q.data_ptr(), o.data_ptr(), seq_lens.data_ptr(),
-                                   batch, Hq, limit, float(tau), float(scale),
-                                   int(bool(per_head)), _ptr(kept), _ptr(bits), _paged_stream(stream, cache._index))
-    _raise(code, "mala_decode_paged")
+    code = lib().mala_decode_paged(cache._ref, q.data_ptr(), o.data_ptr(), lens, batch, Hq, limit,
+                                   tau, scale, 1 if per_head else 0, _ptr(kept), _ptr(bits),
+                                   _paged_stream(stream, cache._index))
+    if code:
+        _raise(code, "mala_decode_paged")
     return (o, kept, bits) if trace else o
 
 
@@ -652,25 +662,24 @@ def mala_cache_gather(cache, cu_seqlens_k, max_seqlen: int, total: int, out=None
     """Reads sequences of a PagedCache back as packed bf16 (K, V), [total, Hkv, 128]
     each, the form mala_fwd_varlen takes: positions 0 .. n_b - 1 of sequence b, n_b =
     cu_seqlens_k[b+1] - cu_seqlens_k[b] <= max_seqlen. ``out``: a (K, V) pair to fill."""
-    torch = _torch()
-    _paged_ready(cache)
-    _check_lens(cache, cu_seqlens_k, "cu_seqlens_k")
-    batch = cu_seqlens_k.shape[0] - 1
+    torch = _paged_ready(cache)
+    cu, entries = _check_lens(torch, cache, cu_seqlens_k, "cu_seqlens_k")
+    batch = entries - 1
     _check_batch(cache, batch)
     total, max_seqlen = int(total), int(max_seqlen)
     if total < 0 or max_seqlen < 0:
         raise ValueError("total and max_seqlen must not be negative")
-    shape = (total, cache.Hkv, 128)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=cache._device)
-                    for _ in range(2))
-    k, v = out
-    _buf(k, "K", cache._device, torch.bfloat16, shape)
-    _buf(v, "V", cache._device, torch.bfloat16, shape)
-    code = lib().mala_cache_gather(cache._ref, k.data_ptr(), v.data_ptr(),
-                                   cu_seqlens_k.data_ptr(), batch, max_seqlen, total,
-                                   _paged_stream(stream, cache._index))
-    _raise(code, "mala_cache_gather")
+        k = cache._tensors[2].new_empty((total, cache.Hkv, 128), dtype=torch.bfloat16)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+        for t, name in ((k, "K"), (v, "V")):
+            _buf(t, name, cache._device, torch.bfloat16, (total, cache.Hkv, 128))
+    code = lib().mala_cache_gather(cache._ref, k.data_ptr(), v.data_ptr(), cu, batch, max_seqlen,
+                                   total, _paged_stream(stream, cache._index))
+    if code:
+        _raise(code, "mala_cache_gather")
     return k, v
 
 

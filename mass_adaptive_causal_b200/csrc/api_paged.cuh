@@ -2,6 +2,8 @@
 // checks and launches (the contract is in include/mala.h).
 #pragma once
 
+#include <atomic>
+
 #include "api.cuh"
 #include "decode_paged_sm100.cuh"
 #include "paged.cuh"
@@ -85,6 +87,27 @@ inline int decode_cluster(const pdec::Params& p, long long groups, bool rule, si
     *smem = need;
   }
   return best;
+}
+
+// What a decode kernel may use, said once per device: three calls of the runtime for
+// each step would be a tenth of its host time.
+inline bool allow_decode(pdec::Kernel kernel, bool wide, bool rule) {
+  static std::atomic<unsigned long long> said[2][2];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  std::atomic<unsigned long long>& mine = said[wide][rule];
+  if (mine.load(std::memory_order_relaxed) & bit) return true;
+  // the carve-out: without it an SM takes one block, although the shared memory of two fits
+  const bool ok =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)pdec::MAX_SMEM) == cudaSuccess &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+          cudaSuccess &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+  if (ok) mine.fetch_or(bit, std::memory_order_relaxed);
+  return ok;
 }
 
 // An input or output of append: [total][heads][128] bf16 by its strides.
@@ -195,12 +218,7 @@ mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q, void
   // a single tile is always kept: exact attention is the rule's answer
   const bool rule = tau > 0.f && p.max_tiles > 1;
   const mala::pdec::Kernel kernel = mala::pdec::decode_kernel_of(p.G, rule);
-  MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)mala::pdec::MAX_SMEM));
-  MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-  // without this an SM takes one block, although the shared memory of two fits
-  MALA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                     cudaSharedmemCarveoutMaxShared));
+  if (!allow_decode(kernel, p.G > 4, rule)) return MALA_ERR_CUDA;
   size_t smem;
   p.C = decode_cluster(p, (long long)batch * Hkv, rule, &smem);
   if (p.C < 1) return MALA_ERR_TOO_LARGE;
