@@ -168,14 +168,36 @@ mala_status mala_cache_append(const mala_paged_cache* cache, const void* k, int6
   p.max_new = max_new < total ? max_new : total;
   const int page = cache->page_size;
   // n consecutive positions lie in at most (n + page - 2) / page + 1 pages
-  const dim3 grid((unsigned)(((long long)p.max_new + page - 2) / page + 1), batch, Hkv);
+  const long long pages = ((long long)p.max_new + page - 2) / page + 1;
+  const int rows = page < p.max_new ? page : p.max_new;  // new ones of a page
+  const int half = p.rot / 2;
   cudaStream_t s = as_stream(stream);
-  if (page <= 32)
-    mala::paged::append_kernel<1><<<grid, mala::paged::APPEND_NT, 0, s>>>(p);
-  else if (page == 64)
-    mala::paged::append_kernel<2><<<grid, mala::paged::APPEND_NT, 0, s>>>(p);
-  else
-    mala::paged::append_kernel<4><<<grid, mala::paged::APPEND_NT, 0, s>>>(p);
+  // A block's heads: all when there are pages enough to fill the chip four times, so that they
+  // share the angles; of decode steps as many as make 32 units of eight threads.
+  int groups = 1;
+  if (rows <= 4) {
+    const int each = 32 / (2 + p.G) > 1 ? 32 / (2 + p.G) : 1;
+    groups = (Hkv + each - 1) / each;
+  } else {
+    const long long blocks = (long long)batch * pages, want = 4ll * sm_count();
+    if (blocks < want) groups = (int)((want + blocks - 1) / blocks);
+  }
+  groups = groups < Hkv ? groups : Hkv;
+  p.heads = (Hkv + groups - 1) / groups;
+  const dim3 grid((unsigned)pages, batch, (Hkv + p.heads - 1) / p.heads);
+  const size_t table = half > 0 && rows > 4 ? (size_t)rows * 32 * sizeof(float4) : 0;
+  constexpr int NT = mala::paged::APPEND_NT;
+  if (rows <= 4) {
+    mala::paged::append_kernel<8, 4><<<grid, NT, 0, s>>>(p);
+  } else if (rows <= 32) {
+    mala::paged::append_kernel<32, 8><<<grid, NT, table, s>>>(p);
+  } else if (rows <= 64) {
+    mala::paged::append_kernel<64, 8><<<grid, NT, table, s>>>(p);
+  } else {
+    MALA_CUDA_TRY(cudaFuncSetAttribute(mala::paged::append_kernel<128, 8>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)table));
+    mala::paged::append_kernel<128, 8><<<grid, NT, table, s>>>(p);
+  }
   return launch_status();
 }
 

@@ -109,12 +109,12 @@ struct AppendParams {
   const int32_t* cu;        // [batch + 1] or null: one new token per sequence
   const int32_t* seq_lens;  // [batch], new tokens included
   const float* inv_freq;    // [rot / 2]
-  int rot, interleaved, G, total, max_new;
+  int rot, interleaved, G, total, max_new, heads;  // heads: key/value heads of a block
 };
 
 constexpr int APPEND_NT = 256;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& u, float* x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -142,8 +142,8 @@ __device__ __forceinline__ Chunks chunks_of(int t, int rot, int interleaved) {
   }
   return c;
 }
-__device__ __forceinline__ void rotate(float (&x)[16], const float (&cs)[8], const float (&sn)[8],
-                                       int interleaved) {
+// cs[j] = cos and sin of frequencies 2 j and 2 j + 1 of the thread's eight.
+__device__ __forceinline__ void rotate(float (&x)[16], const float4 (&cs)[4], int interleaved) {
   auto pair = [](float& a, float& b, float c, float s) {
     const float xa = a, xb = b;
     a = fmaf(xa, c, -xb * s);
@@ -151,89 +151,50 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float (&cs)[8], con
   };
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) pair(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
+    for (int j = 0; j < 4; ++j) {
+      pair(x[4 * j], x[4 * j + 1], cs[j].x, cs[j].y);
+      pair(x[4 * j + 2], x[4 * j + 3], cs[j].z, cs[j].w);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) pair(x[i], x[i + 8], cs[i], sn[i]);
-  }
-}
-
-__device__ __forceinline__ float block_max(float x, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = red[0];
-#pragma unroll
-  for (int w = 1; w < APPEND_NT / 32; ++w) x = fmaxf(x, red[w]);
-  return x;
-}
-
-// Writes the rows [row0, row0 + n) of one page and head, whose values this
-// block's threads hold (x[pass], rows `tid / 8 + 32 * pass`), and settles the
-// page's scale. The rows below row0 hold earlier tokens.
-template <int PASSES>
-__device__ __forceinline__ void store_page(uint8_t* base, long long tok, float* scale, int row0,
-                                           int n, const Chunks& ch, float (&x)[PASSES][16],
-                                           float* red) {
-  const int r0 = threadIdx.x >> 3;
-  float amax = 0.f;
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float a = fabsf(x[p][i]);
-      if (a < __int_as_float(0x7f800000)) amax = fmaxf(amax, a);
-      else x[p][i] = __int_as_float(0x7fc00000);  // e4m3 has no infinities
+    for (int j = 0; j < 4; ++j) {
+      pair(x[2 * j], x[2 * j + 8], cs[j].x, cs[j].y);
+      pair(x[2 * j + 1], x[2 * j + 9], cs[j].z, cs[j].w);
     }
-  amax = block_max(amax, red);
-  float s = pow2_scale(amax);
-  if (row0 > 0) {
-    const float old = *scale;
-    if (old >= s) {
-      s = old;
-    } else {
-      const float ratio = old / s;
-      for (int e = threadIdx.x; e < row0 * 8; e += APPEND_NT) {
-        uint4* at = reinterpret_cast<uint4*>(base + (e >> 3) * tok + (e & 7) * 16);
-        uint4 u = *at;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 lo = f16x2_to_float2(e4m3x2_to_f16x2(w[i]));
-          const float2 hi = f16x2_to_float2(e4m3x2_hi_to_f16x2(w[i]));
-          w[i] = floats_to_e4m3x2(lo.x * ratio, lo.y * ratio) |
-                 floats_to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16;
-        }
-        *at = u;
-      }
-    }
-    __syncthreads();  // every thread has read the old scale
-  }
-  if (threadIdx.x == 0) *scale = s;
-  const float inv = 1.f / s;
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    const int r = r0 + 32 * p;
-    if (r >= n) continue;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = floats_to_e4m3x2(x[p][4 * i] * inv, x[p][4 * i + 1] * inv) |
-             floats_to_e4m3x2(x[p][4 * i + 2] * inv, x[p][4 * i + 3] * inv) << 16;
-    uint8_t* row = base + (row0 + r) * tok;
-    *reinterpret_cast<uint2*>(row + ch.c0) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(row + ch.c1) = make_uint2(w[2], w[3]);
   }
 }
 
-// One block per (page of new tokens, sequence, key/value head): rotates and
-// stores the page's new K and V rows and rotates the head's G query heads.
-template <int PASSES>
-__global__ void __launch_bounds__(APPEND_NT) append_kernel(const AppendParams p) {
+// Sixteen e4m3 values that lay under another scale: times ratio, rounded again.
+__device__ __forceinline__ void rescale16(uint8_t* p, float ratio) {
+  uint4 u = *reinterpret_cast<const uint4*>(p);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 lo = f16x2_to_float2(e4m3x2_to_f16x2(w[i]));
+    const float2 hi = f16x2_to_float2(e4m3x2_hi_to_f16x2(w[i]));
+    w[i] = floats_to_e4m3x2(lo.x * ratio, lo.y * ratio) |
+           floats_to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16;
+  }
+  *reinterpret_cast<uint4*>(p) = u;
+}
+
+// One block per (page of new tokens, sequence, group of key/value heads). Its units are the
+// new rows of one head: K and V (rotate, find the page's scale, round, store) and Q
+// (rotate, store). A unit is LPU threads' work, eight of them a row, each thread holding
+// PASSES rows' sixteen values as they were loaded, so that a page's largest value is known
+// before the first one is rounded and everything is read once; the rotation is done twice
+// instead (32 FMA a row and thread, a tenth of the time that the bytes take). LPU and
+// PASSES follow the rows that a page can get (host): up to 4 (decode steps): 8 threads, the
+// angles in registers; up to 32, 64, 128: one, two, four warps, the angles in shared memory
+// for all heads of the block. 4 x 8192 tokens, pages of 128: see the launch.
+template <int LPU, int PASSES>
+__global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams p) {
+  constexpr int UNITS = APPEND_NT / LPU;  // side by side
+  constexpr int STEP = LPU / 8;           // rows side by side
+  constexpr bool TABLE = LPU > 8;
+  extern __shared__ float4 table[];       // [row][4][8]: cs of thread t's j-th pair at [j][t]
   __shared__ float red[APPEND_NT / 32];
-  const int b = blockIdx.y, h = blockIdx.z;
+  const int b = blockIdx.y;
   int first = b, count = 1;
   if (p.cu) {
     first = p.cu[b];
@@ -246,94 +207,179 @@ __global__ void __launch_bounds__(APPEND_NT) append_kernel(const AppendParams p)
     return;
   }
   const int start = len - count;
-  const int page = p.pool.page;
-  const int slot = start / page + blockIdx.x;
-  const int begin = max(start, slot * page), end = min(len, (slot + 1) * page);
+  const int slot = (start >> p.pool.page_log2) + blockIdx.x;
+  const int begin = max(start, slot << p.pool.page_log2);
+  const int end = (int)min((long long)len, (long long)(slot + 1) << p.pool.page_log2);
   if (begin >= end) return;
-  const int row0 = begin - slot * page, n = end - begin;
-  const int t = threadIdx.x & 7, r0 = threadIdx.x >> 3;
-  const Chunks ch = chunks_of(t, p.rot, p.interleaved);
+  const int row0 = begin - (slot << p.pool.page_log2), n = end - begin;
   const long long tok0 = (long long)first + (begin - start);
+  const int tid = threadIdx.x, t = tid & 7, r0 = (tid % LPU) >> 3;
+  const Chunks ch = chunks_of(t, p.rot, p.interleaved);
+  const int h0 = blockIdx.z * p.heads, nh = min(p.heads, p.pool.Hkv - h0);
+  const int id = page_of(p.pool, b, slot);  // no page: its rows are left out, q is rotated all the same
 
-  float freq[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) freq[i] = ch.freq >= 0 ? p.inv_freq[ch.freq + i] : 0.f;
-  float x[PASSES][16];
-#pragma unroll
-  for (int ps = 0; ps < PASSES; ++ps) {
-    const int r = r0 + 32 * ps;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[ps][i] = 0.f;
-    if (r >= n) continue;
-    const __nv_bfloat16* row = p.k + (tok0 + r) * p.k_tok + h * p.k_head;
-    float lo[8], hi[8];
-    unpack8(*reinterpret_cast<const uint4*>(row + ch.c0), lo);
-    unpack8(*reinterpret_cast<const uint4*>(row + ch.c1), hi);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[ps][i] = lo[i];
-      x[ps][8 + i] = hi[i];
+  if (TABLE && p.rot > 0) {
+    const int half = p.rot >> 1;
+    for (int e = tid; e < n * (half / 2); e += APPEND_NT) {
+      const int r = e / (half / 2), f = 2 * (e - r * (half / 2));
+      float4 cs;
+      turn(begin + r, p.inv_freq[f], cs.x, cs.y);
+      turn(begin + r, p.inv_freq[f + 1], cs.z, cs.w);
+      table[r * 32 + ((f >> 1) & 3) * 8 + (f >> 3)] = cs;
     }
-    float cs[8], sn[8];
-    if (ch.freq >= 0) {
+    __syncthreads();
+  }
+  float4 own[TABLE ? 1 : PASSES][4];
+  if (!TABLE && ch.freq >= 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) turn(begin + r, freq[i], cs[i], sn[i]);
-      rotate(x[ps], cs, sn, p.interleaved);
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = make_float2(p.inv_freq[ch.freq + 2 * j], p.inv_freq[ch.freq + 2 * j + 1]);
+#pragma unroll
+      for (int ps = 0; ps < (TABLE ? 1 : PASSES); ++ps)
+        if (ps < n) {
+          turn(begin + ps, f.x, own[ps][j].x, own[ps][j].y);
+          turn(begin + ps, f.y, own[ps][j].z, own[ps][j].w);
+        }
     }
-    if (p.q) {
-      for (int g = 0; g < p.G; ++g) {
-        const int hq = h * p.G + g;
-        const __nv_bfloat16* qr = p.q + (tok0 + r) * p.q_tok + hq * p.q_head;
-        __nv_bfloat16* qo = p.q_out + (tok0 + r) * p.qo_tok + hq * p.qo_head;
-        const uint4 u0 = *reinterpret_cast<const uint4*>(qr + ch.c0);
-        const uint4 u1 = *reinterpret_cast<const uint4*>(qr + ch.c1);
-        if (ch.freq < 0) {
-          *reinterpret_cast<uint4*>(qo + ch.c0) = u0;
-          *reinterpret_cast<uint4*>(qo + ch.c1) = u1;
-          continue;
-        }
-        float y[16];
-        unpack8(u0, lo);
-        unpack8(u1, hi);
+  }
+  auto angles = [&](int ps, int r, float4 (&cs)[4]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = lo[i];
-          y[8 + i] = hi[i];
+    for (int j = 0; j < 4; ++j) cs[j] = TABLE ? table[r * 32 + j * 8 + t] : own[TABLE ? 0 : ps][j];
+  };
+
+  const int total = nh * (2 + p.G);  // K of every head, V of every head, Q
+  for (int u0 = 0; u0 < total; u0 += UNITS) {
+    const int u = u0 + tid / LPU;
+    const bool live = u < total;
+    const int kind = u < nh ? 0 : (u < 2 * nh ? 1 : 2);
+    const bool rotates = kind != 1 && ch.freq >= 0;
+    const __nv_bfloat16* src = p.k + (h0 + u) * p.k_head + tok0 * p.k_tok;
+    long long stride = p.k_tok;
+    if (kind == 1) {
+      src = p.v + (h0 + u - nh) * p.v_head + tok0 * p.v_tok;
+      stride = p.v_tok;
+    } else if (kind == 2) {
+      src = p.q + ((long long)h0 * p.G + (u - 2 * nh)) * p.q_head + tok0 * p.q_tok;
+      stride = p.q_tok;
+    }
+    uint4 raw[PASSES][2];
+#pragma unroll
+    for (int ps = 0; ps < PASSES; ++ps) {
+      const int r = r0 + STEP * ps;
+      raw[ps][0] = raw[ps][1] = make_uint4(0, 0, 0, 0);
+      if (live && r < n && (kind == 2 || id >= 0)) {
+        raw[ps][0] = *reinterpret_cast<const uint4*>(src + r * stride + ch.c0);
+        raw[ps][1] = *reinterpret_cast<const uint4*>(src + r * stride + ch.c1);
+      }
+    }
+    const bool kv = live && kind < 2 && id >= 0;
+    const int h = h0 + (kind == 0 ? u : u - nh);
+    uint8_t* base = kind == 0 ? p.pool.k + id * p.pool.k_page + h * p.pool.k_head
+                              : p.pool.v + id * p.pool.v_page + h * p.pool.v_head;
+    const long long tok = kind == 0 ? p.pool.k_tok : p.pool.v_tok;
+    float* scale = (kind == 0 ? p.pool.k_scale : p.pool.v_scale) + (long long)id * p.pool.Hkv + h;
+    const float old = kv && row0 > 0 ? *scale : 0.f;  // read by all before it is written below
+    float amax = 0.f;
+    if (kv) {
+#pragma unroll
+      for (int ps = 0; ps < PASSES; ++ps) {
+        if (r0 + STEP * ps >= n) continue;
+        float x[16];
+        unpack8(raw[ps][0], x);
+        unpack8(raw[ps][1], x + 8);
+        if (rotates) {
+          float4 cs[4];
+          angles(ps, r0 + STEP * ps, cs);
+          rotate(x, cs, p.interleaved);
         }
-        rotate(y, cs, sn, p.interleaved);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float a = fabsf(x[i]);
+          if (a < __int_as_float(0x7f800000)) amax = fmaxf(amax, a);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < (LPU < 32 ? LPU : 32); d <<= 1)
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    if (LPU > 32) {
+      __syncthreads();
+      if ((tid & 31) == 0) red[tid >> 5] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < LPU / 32; ++w) amax = fmaxf(amax, red[(tid / LPU) * (LPU / 32) + w]);
+    }
+    float s = pow2_scale(amax), ratio = 0.f;
+    bool grown = false;
+    if (kv && row0 > 0) {
+      if (old >= s) {
+        s = old;
+      } else {
+        grown = true;
+        ratio = old / s;
+      }
+    }
+    if (kv && tid % LPU == 0) *scale = s;
+    if (LPU >= 32) {
+      if (grown)
+        for (int e = tid % LPU; e < row0 * 8; e += LPU) rescale16(base + (e >> 3) * tok + (e & 7) * 16, ratio);
+    } else {  // the whole warp, one of its units after the other
+      uint32_t todo = __ballot_sync(0xffffffffu, grown && tid % LPU == 0);
+      while (todo) {
+        const int lane = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const unsigned long long at =
+            __shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)base, lane);
+        const long long step = __shfl_sync(0xffffffffu, tok, lane);
+        const float by = __shfl_sync(0xffffffffu, ratio, lane);
+#pragma unroll 4
+        for (int e = tid & 31; e < row0 * 8; e += 32)
+          rescale16(reinterpret_cast<uint8_t*>((uintptr_t)at) + (e >> 3) * step + (e & 7) * 16, by);
+      }
+    }
+    const float inv = 1.f / s;
+    __nv_bfloat16* dst = p.q_out + ((long long)h0 * p.G + (u - 2 * nh)) * p.qo_head + tok0 * p.qo_tok;
+#pragma unroll
+    for (int ps = 0; ps < PASSES; ++ps) {
+      const int r = r0 + STEP * ps;
+      if (!live || r >= n) continue;
+      if (kind == 2 && ch.freq < 0) {  // bit for bit
+        *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c0) = raw[ps][0];
+        *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c1) = raw[ps][1];
+        continue;
+      }
+      float x[16];
+      unpack8(raw[ps][0], x);
+      unpack8(raw[ps][1], x + 8);
+      if (rotates) {
+        float4 cs[4];
+        angles(ps, r, cs);
+        rotate(x, cs, p.interleaved);
+      }
+      if (kind == 2) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const __nv_bfloat162 z = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+          const __nv_bfloat162 z = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
           w[i] = *reinterpret_cast<const uint32_t*>(&z);
         }
-        *reinterpret_cast<uint4*>(qo + ch.c0) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(qo + ch.c1) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c0) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c1) = make_uint4(w[4], w[5], w[6], w[7]);
+      } else if (kv) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)  // e4m3 has no infinities
+          if (!(fabsf(x[i]) < __int_as_float(0x7f800000))) x[i] = __int_as_float(0x7fc00000);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = floats_to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
+                 floats_to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
+        uint8_t* row = base + (row0 + r) * tok;
+        *reinterpret_cast<uint2*>(row + ch.c0) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(row + ch.c1) = make_uint2(w[2], w[3]);
       }
     }
   }
-  const int id = page_of(p.pool, b, slot);
-  if (id < 0) return;
-  store_page<PASSES>(p.pool.k + id * p.pool.k_page + h * p.pool.k_head, p.pool.k_tok,
-                     p.pool.k_scale + (long long)id * p.pool.Hkv + h, row0, n, ch, x, red);
-#pragma unroll
-  for (int ps = 0; ps < PASSES; ++ps) {
-    const int r = r0 + 32 * ps;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[ps][i] = 0.f;
-    if (r >= n) continue;
-    const __nv_bfloat16* row = p.v + (tok0 + r) * p.v_tok + h * p.v_head;
-    float lo[8], hi[8];
-    unpack8(*reinterpret_cast<const uint4*>(row + ch.c0), lo);
-    unpack8(*reinterpret_cast<const uint4*>(row + ch.c1), hi);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[ps][i] = lo[i];
-      x[ps][8 + i] = hi[i];
-    }
-  }
-  store_page<PASSES>(p.pool.v + id * p.pool.v_page + h * p.pool.v_head, p.pool.v_tok,
-                     p.pool.v_scale + (long long)id * p.pool.Hkv + h, row0, n, ch, x, red);
 }
 
 struct GatherParams {
