@@ -162,7 +162,6 @@ mala_status mala_cache_append(const mala_paged_cache* cache, const void* k, int6
   p.seq_lens = seq_lens;
   p.inv_freq = inv_freq;
   p.rot = rot_dim;
-  p.interleaved = interleaved;
   p.G = q ? Hq / Hkv : 0;
   p.total = total;
   p.max_new = max_new < total ? max_new : total;
@@ -175,7 +174,7 @@ mala_status mala_cache_append(const mala_paged_cache* cache, const void* k, int6
   // A block's heads: all when there are pages enough to fill the chip four times, so that they
   // share the angles; of decode steps as many as make 32 units of eight threads.
   int groups = 1;
-  if (rows <= 4) {
+  if (rows <= 2) {
     const int each = 32 / (2 + p.G) > 1 ? 32 / (2 + p.G) : 1;
     groups = (Hkv + each - 1) / each;
   } else {
@@ -185,19 +184,12 @@ mala_status mala_cache_append(const mala_paged_cache* cache, const void* k, int6
   groups = groups < Hkv ? groups : Hkv;
   p.heads = (Hkv + groups - 1) / groups;
   const dim3 grid((unsigned)pages, batch, (Hkv + p.heads - 1) / p.heads);
-  const size_t table = half > 0 && rows > 4 ? (size_t)rows * 32 * sizeof(float4) : 0;
-  constexpr int NT = mala::paged::APPEND_NT;
-  if (rows <= 4) {
-    mala::paged::append_kernel<8, 4><<<grid, NT, 0, s>>>(p);
-  } else if (rows <= 32) {
-    mala::paged::append_kernel<32, 8><<<grid, NT, table, s>>>(p);
-  } else if (rows <= 64) {
-    mala::paged::append_kernel<64, 8><<<grid, NT, table, s>>>(p);
-  } else {
-    MALA_CUDA_TRY(cudaFuncSetAttribute(mala::paged::append_kernel<128, 8>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)table));
-    mala::paged::append_kernel<128, 8><<<grid, NT, table, s>>>(p);
-  }
+  const size_t table = half > 0 && rows > 2 ? (size_t)rows * 32 * sizeof(float4) : 0;
+  const mala::paged::AppendKernel kernel = mala::paged::append_kernel_of(rows, interleaved != 0);
+  if (table > 48 * 1024)
+    MALA_CUDA_TRY(
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)table));
+  kernel<<<grid, mala::paged::APPEND_NT, table, s>>>(p);
   return launch_status();
 }
 

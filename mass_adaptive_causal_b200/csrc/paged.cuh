@@ -109,7 +109,7 @@ struct AppendParams {
   const int32_t* cu;        // [batch + 1] or null: one new token per sequence
   const int32_t* seq_lens;  // [batch], new tokens included
   const float* inv_freq;    // [rot / 2]
-  int rot, interleaved, G, total, max_new, heads;  // heads: key/value heads of a block
+  int rot, G, total, max_new, heads;  // heads: key/value heads of a block
 };
 
 constexpr int APPEND_NT = 256;
@@ -142,25 +142,47 @@ __device__ __forceinline__ Chunks chunks_of(int t, int rot, int interleaved) {
   }
   return c;
 }
-// cs[j] = cos and sin of frequencies 2 j and 2 j + 1 of the thread's eight.
-__device__ __forceinline__ void rotate(float (&x)[16], const float4 (&cs)[4], int interleaved) {
-  auto pair = [](float& a, float& b, float c, float s) {
-    const float xa = a, xb = b;
-    a = fmaf(xa, c, -xb * s);
-    b = fmaf(xb, c, xa * s);
-  };
-  if (interleaved) {
+// Two floats side by side, and the two-at-a-time instructions on them.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split2(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// cs[j] = cos, cos, sin, sin of the thread's frequencies 2 j and 2 j + 1. Each result is a
+// product rounded and a sum of products rounded once.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate(float (&x)[16], const float4 (&cs)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      pair(x[4 * j], x[4 * j + 1], cs[j].x, cs[j].y);
-      pair(x[4 * j + 2], x[4 * j + 3], cs[j].z, cs[j].w);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      pair(x[2 * j], x[2 * j + 8], cs[j].x, cs[j].y);
-      pair(x[2 * j + 1], x[2 * j + 9], cs[j].z, cs[j].w);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 c = pack2(cs[j].x, cs[j].y), s = pack2(cs[j].z, cs[j].w);
+    const f32x2 minus = mul2(s, pack2(-1.f, -1.f));
+    // the pairs' first and second elements
+    constexpr int A = INTERLEAVED ? 4 : 2, STEP = INTERLEAVED ? 2 : 1, B = INTERLEAVED ? 1 : 8;
+    const f32x2 a = pack2(x[A * j], x[A * j + STEP]);
+    const f32x2 b = pack2(x[A * j + B], x[A * j + STEP + B]);
+    const float2 ra = split2(fma2(b, minus, mul2(a, c)));
+    const float2 rb = split2(fma2(a, s, mul2(b, c)));
+    x[A * j] = ra.x;
+    x[A * j + STEP] = ra.y;
+    x[A * j + B] = rb.x;
+    x[A * j + STEP + B] = rb.y;
   }
 }
 
@@ -182,18 +204,19 @@ __device__ __forceinline__ void rescale16(uint8_t* p, float ratio) {
 // new rows of one head: K and V (rotate, find the page's scale, round, store) and Q
 // (rotate, store). A unit is LPU threads' work, eight of them a row, each thread holding
 // PASSES rows' sixteen values as they were loaded, so that a page's largest value is known
-// before the first one is rounded and everything is read once; the rotation is done twice
-// instead (32 FMA a row and thread, a tenth of the time that the bytes take). LPU and
-// PASSES follow the rows that a page can get (host): up to 4 (decode steps): 8 threads, the
-// angles in registers; up to 32, 64, 128: one, two, four warps, the angles in shared memory
-// for all heads of the block. 4 x 8192 tokens, pages of 128: see the launch.
-template <int LPU, int PASSES>
+// before the first one is rounded and everything is read once; K is rotated twice instead. As
+// soon as a row is stored, the next unit's takes its registers, so loads are always under way.
+// LPU and PASSES follow the rows that a page can get (host): up to 2 (decode steps): 8 threads,
+// the angles in registers; up to 32, 64, 128: one, two, four warps, the angles in shared
+// memory for all heads of the block.
+template <int LPU, int PASSES, bool INTERLEAVED>
 __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams p) {
   constexpr int UNITS = APPEND_NT / LPU;  // side by side
   constexpr int STEP = LPU / 8;           // rows side by side
   constexpr bool TABLE = LPU > 8;
-  extern __shared__ float4 table[];       // [row][4][8]: cs of thread t's j-th pair at [j][t]
+  extern __shared__ float4 table[];       // [row][4][8]: cs[j] of thread t at [j][t]
   __shared__ float red[APPEND_NT / 32];
+  const float inf = __int_as_float(0x7f800000);
   const int b = blockIdx.y;
   int first = b, count = 1;
   if (p.cu) {
@@ -214,17 +237,45 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
   const int row0 = begin - (slot << p.pool.page_log2), n = end - begin;
   const long long tok0 = (long long)first + (begin - start);
   const int tid = threadIdx.x, t = tid & 7, r0 = (tid % LPU) >> 3;
-  const Chunks ch = chunks_of(t, p.rot, p.interleaved);
+  const Chunks ch = chunks_of(t, p.rot, INTERLEAVED);
   const int h0 = blockIdx.z * p.heads, nh = min(p.heads, p.pool.Hkv - h0);
   const int id = page_of(p.pool, b, slot);  // no page: its rows are left out, q is rotated all the same
 
+  // the units: K of every head, V of every head, Q
+  const int total = nh * (2 + p.G);
+  const __nv_bfloat16* src = nullptr;
+  long long stride = 0;
+  auto aim = [&](int u) {
+    if (u < nh) {
+      src = p.k + (h0 + u) * p.k_head + tok0 * p.k_tok;
+      stride = p.k_tok;
+    } else if (u < 2 * nh) {
+      src = p.v + (h0 + u - nh) * p.v_head + tok0 * p.v_tok;
+      stride = p.v_tok;
+    } else {
+      src = p.q + ((long long)h0 * p.G + (u - 2 * nh)) * p.q_head + tok0 * p.q_tok;
+      stride = p.q_tok;
+    }
+  };
+  uint4 raw[PASSES][2];
+  auto load = [&](int ps, bool live) {
+    const int r = r0 + STEP * ps;
+    if (live && r < n) {
+      raw[ps][0] = *reinterpret_cast<const uint4*>(src + r * stride + ch.c0);
+      raw[ps][1] = *reinterpret_cast<const uint4*>(src + r * stride + ch.c1);
+    }
+  };
+  aim(tid / LPU);
+#pragma unroll
+  for (int ps = 0; ps < PASSES; ++ps) load(ps, tid / LPU < total);
+
   if (TABLE && p.rot > 0) {
-    const int half = p.rot >> 1;
-    for (int e = tid; e < n * (half / 2); e += APPEND_NT) {
-      const int r = e / (half / 2), f = 2 * (e - r * (half / 2));
+    const int quarter = p.rot >> 2;
+    for (int e = tid; e < n * quarter; e += APPEND_NT) {
+      const int r = e / quarter, f = 2 * (e - r * quarter);
       float4 cs;
-      turn(begin + r, p.inv_freq[f], cs.x, cs.y);
-      turn(begin + r, p.inv_freq[f + 1], cs.z, cs.w);
+      turn(begin + r, p.inv_freq[f], cs.x, cs.z);
+      turn(begin + r, p.inv_freq[f + 1], cs.y, cs.w);
       table[r * 32 + ((f >> 1) & 3) * 8 + (f >> 3)] = cs;
     }
     __syncthreads();
@@ -237,149 +288,154 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
 #pragma unroll
       for (int ps = 0; ps < (TABLE ? 1 : PASSES); ++ps)
         if (ps < n) {
-          turn(begin + ps, f.x, own[ps][j].x, own[ps][j].y);
-          turn(begin + ps, f.y, own[ps][j].z, own[ps][j].w);
+          turn(begin + ps, f.x, own[ps][j].x, own[ps][j].z);
+          turn(begin + ps, f.y, own[ps][j].y, own[ps][j].w);
         }
     }
   }
-  auto angles = [&](int ps, int r, float4 (&cs)[4]) {
+  // a row's values in float32, rotated
+  auto values = [&](int ps, bool rotates, float (&x)[16]) {
+    unpack8(raw[ps][0], x);
+    unpack8(raw[ps][1], x + 8);
+    if (!rotates) return;
+    float4 cs[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cs[j] = TABLE ? table[r * 32 + j * 8 + t] : own[TABLE ? 0 : ps][j];
+    for (int j = 0; j < 4; ++j)
+      cs[j] = TABLE ? table[(r0 + STEP * ps) * 32 + j * 8 + t] : own[TABLE ? 0 : ps][j];
+    rotate<INTERLEAVED>(x, cs);
   };
 
-  const int total = nh * (2 + p.G);  // K of every head, V of every head, Q
   for (int u0 = 0; u0 < total; u0 += UNITS) {
     const int u = u0 + tid / LPU;
-    const bool live = u < total;
-    const int kind = u < nh ? 0 : (u < 2 * nh ? 1 : 2);
-    const bool rotates = kind != 1 && ch.freq >= 0;
-    const __nv_bfloat16* src = p.k + (h0 + u) * p.k_head + tok0 * p.k_tok;
-    long long stride = p.k_tok;
-    if (kind == 1) {
-      src = p.v + (h0 + u - nh) * p.v_head + tok0 * p.v_tok;
-      stride = p.v_tok;
-    } else if (kind == 2) {
-      src = p.q + ((long long)h0 * p.G + (u - 2 * nh)) * p.q_head + tok0 * p.q_tok;
-      stride = p.q_tok;
-    }
-    uint4 raw[PASSES][2];
+    const bool more = u + UNITS < total;
+    aim(u + UNITS);
+    const bool kv = u < 2 * nh, keys = u < nh;
+    const bool rotates = (keys || !kv) && ch.freq >= 0;
+    if (u0 < 2 * nh) {  // some of the block's units are K or V
+      const bool store = kv && id >= 0;
+      const int h = h0 + (keys ? u : u - nh);
+      uint8_t* base = keys ? p.pool.k + id * p.pool.k_page + h * p.pool.k_head
+                           : p.pool.v + id * p.pool.v_page + h * p.pool.v_head;
+      const long long tok = keys ? p.pool.k_tok : p.pool.v_tok;
+      float* scale = (keys ? p.pool.k_scale : p.pool.v_scale) + (long long)id * p.pool.Hkv + h;
+      const float old = store && row0 > 0 ? *scale : 0.f;  // read by all before it is written below
+      auto largest = [&](bool finite) {
+        float m = 0.f;
+        if (store) {
 #pragma unroll
-    for (int ps = 0; ps < PASSES; ++ps) {
-      const int r = r0 + STEP * ps;
-      raw[ps][0] = raw[ps][1] = make_uint4(0, 0, 0, 0);
-      if (live && r < n && (kind == 2 || id >= 0)) {
-        raw[ps][0] = *reinterpret_cast<const uint4*>(src + r * stride + ch.c0);
-        raw[ps][1] = *reinterpret_cast<const uint4*>(src + r * stride + ch.c1);
+          for (int ps = 0; ps < PASSES; ++ps) {
+            if (r0 + STEP * ps >= n) continue;
+            float x[16];
+            values(ps, rotates, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)  // a NaN is passed over
+              m = fmaxf(m, finite && fabsf(x[i]) == inf ? 0.f : fabsf(x[i]));
+          }
+        }
+#pragma unroll
+        for (int d = 1; d < (LPU < 32 ? LPU : 32); d <<= 1)
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if (LPU > 32) {
+          __syncthreads();
+          if ((tid & 31) == 0) red[tid >> 5] = m;
+          __syncthreads();
+#pragma unroll
+          for (int w = 0; w < LPU / 32; ++w) m = fmaxf(m, red[(tid / LPU) * (LPU / 32) + w]);
+        }
+        return m;
+      };
+      float amax = largest(false);
+      const bool infinite = amax == inf;
+      // once more without the infinities, where there are any
+      if (LPU > 32 ? __syncthreads_or(infinite) : __any_sync(0xffffffffu, infinite))
+        amax = largest(true);
+      float s = pow2_scale(amax), ratio = 0.f;
+      bool grown = false;
+      if (store && row0 > 0) {
+        if (old >= s) {
+          s = old;
+        } else {
+          grown = true;
+          ratio = old / s;
+        }
+      }
+      if (store && tid % LPU == 0) *scale = s;
+      if (LPU >= 32) {
+        if (grown)
+#pragma unroll 4
+          for (int e = tid % LPU; e < row0 * 8; e += LPU)
+            rescale16(base + (e >> 3) * tok + (e & 7) * 16, ratio);
+      } else {  // the whole warp, one of its units after the other
+        uint32_t todo = __ballot_sync(0xffffffffu, grown && tid % LPU == 0);
+        while (todo) {
+          const int lane = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const unsigned long long at =
+              __shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)base, lane);
+          const long long step = __shfl_sync(0xffffffffu, tok, lane);
+          const float by = __shfl_sync(0xffffffffu, ratio, lane);
+#pragma unroll 4
+          for (int e = tid & 31; e < row0 * 8; e += 32)
+            rescale16(reinterpret_cast<uint8_t*>((uintptr_t)at) + (e >> 3) * step + (e & 7) * 16, by);
+        }
+      }
+      const float inv = 1.f / s;
+      if (kv) {
+#pragma unroll
+        for (int ps = 0; ps < PASSES; ++ps) {
+          const int r = r0 + STEP * ps;
+          if (r < n && id >= 0) {
+            float x[16];
+            values(ps, rotates, x);
+            if (infinite)  // e4m3 has none
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (fabsf(x[i]) == inf) x[i] = __int_as_float(0x7fc00000);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = floats_to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
+                     floats_to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
+            uint8_t* row = base + (row0 + r) * tok;
+            *reinterpret_cast<uint2*>(row + ch.c0) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(row + ch.c1) = make_uint2(w[2], w[3]);
+          }
+          load(ps, more);
+        }
       }
     }
-    const bool kv = live && kind < 2 && id >= 0;
-    const int h = h0 + (kind == 0 ? u : u - nh);
-    uint8_t* base = kind == 0 ? p.pool.k + id * p.pool.k_page + h * p.pool.k_head
-                              : p.pool.v + id * p.pool.v_page + h * p.pool.v_head;
-    const long long tok = kind == 0 ? p.pool.k_tok : p.pool.v_tok;
-    float* scale = (kind == 0 ? p.pool.k_scale : p.pool.v_scale) + (long long)id * p.pool.Hkv + h;
-    const float old = kv && row0 > 0 ? *scale : 0.f;  // read by all before it is written below
-    float amax = 0.f;
-    if (kv) {
+    if (!kv && u < total) {
+      __nv_bfloat16* dst = p.q_out + ((long long)h0 * p.G + (u - 2 * nh)) * p.qo_head + tok0 * p.qo_tok;
 #pragma unroll
       for (int ps = 0; ps < PASSES; ++ps) {
-        if (r0 + STEP * ps >= n) continue;
-        float x[16];
-        unpack8(raw[ps][0], x);
-        unpack8(raw[ps][1], x + 8);
-        if (rotates) {
-          float4 cs[4];
-          angles(ps, r0 + STEP * ps, cs);
-          rotate(x, cs, p.interleaved);
+        const int r = r0 + STEP * ps;
+        if (r < n) {
+          uint4 w[2] = {raw[ps][0], raw[ps][1]};  // not rotated: bit for bit
+          if (rotates) {
+            float x[16];
+            values(ps, true, x);
+            uint32_t* z = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+              z[i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+          }
+          *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c0) = w[0];
+          *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c1) = w[1];
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = fabsf(x[i]);
-          if (a < __int_as_float(0x7f800000)) amax = fmaxf(amax, a);
-        }
-      }
-    }
-#pragma unroll
-    for (int d = 1; d < (LPU < 32 ? LPU : 32); d <<= 1)
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    if (LPU > 32) {
-      __syncthreads();
-      if ((tid & 31) == 0) red[tid >> 5] = amax;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < LPU / 32; ++w) amax = fmaxf(amax, red[(tid / LPU) * (LPU / 32) + w]);
-    }
-    float s = pow2_scale(amax), ratio = 0.f;
-    bool grown = false;
-    if (kv && row0 > 0) {
-      if (old >= s) {
-        s = old;
-      } else {
-        grown = true;
-        ratio = old / s;
-      }
-    }
-    if (kv && tid % LPU == 0) *scale = s;
-    if (LPU >= 32) {
-      if (grown)
-        for (int e = tid % LPU; e < row0 * 8; e += LPU) rescale16(base + (e >> 3) * tok + (e & 7) * 16, ratio);
-    } else {  // the whole warp, one of its units after the other
-      uint32_t todo = __ballot_sync(0xffffffffu, grown && tid % LPU == 0);
-      while (todo) {
-        const int lane = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const unsigned long long at =
-            __shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)base, lane);
-        const long long step = __shfl_sync(0xffffffffu, tok, lane);
-        const float by = __shfl_sync(0xffffffffu, ratio, lane);
-#pragma unroll 4
-        for (int e = tid & 31; e < row0 * 8; e += 32)
-          rescale16(reinterpret_cast<uint8_t*>((uintptr_t)at) + (e >> 3) * step + (e & 7) * 16, by);
-      }
-    }
-    const float inv = 1.f / s;
-    __nv_bfloat16* dst = p.q_out + ((long long)h0 * p.G + (u - 2 * nh)) * p.qo_head + tok0 * p.qo_tok;
-#pragma unroll
-    for (int ps = 0; ps < PASSES; ++ps) {
-      const int r = r0 + STEP * ps;
-      if (!live || r >= n) continue;
-      if (kind == 2 && ch.freq < 0) {  // bit for bit
-        *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c0) = raw[ps][0];
-        *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c1) = raw[ps][1];
-        continue;
-      }
-      float x[16];
-      unpack8(raw[ps][0], x);
-      unpack8(raw[ps][1], x + 8);
-      if (rotates) {
-        float4 cs[4];
-        angles(ps, r, cs);
-        rotate(x, cs, p.interleaved);
-      }
-      if (kind == 2) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const __nv_bfloat162 z = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&z);
-        }
-        *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c0) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c1) = make_uint4(w[4], w[5], w[6], w[7]);
-      } else if (kv) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)  // e4m3 has no infinities
-          if (!(fabsf(x[i]) < __int_as_float(0x7f800000))) x[i] = __int_as_float(0x7fc00000);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = floats_to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
-                 floats_to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
-        uint8_t* row = base + (row0 + r) * tok;
-        *reinterpret_cast<uint2*>(row + ch.c0) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2*>(row + ch.c1) = make_uint2(w[2], w[3]);
+        load(ps, more);
       }
     }
   }
+}
+
+using AppendKernel = void (*)(AppendParams);
+inline AppendKernel append_kernel_of(int rows, bool interleaved) {
+  if (rows <= 2) return interleaved ? append_kernel<8, 2, true> : append_kernel<8, 2, false>;
+  if (rows <= 32) return interleaved ? append_kernel<32, 8, true> : append_kernel<32, 8, false>;
+  if (rows <= 64) return interleaved ? append_kernel<64, 8, true> : append_kernel<64, 8, false>;
+  return interleaved ? append_kernel<128, 8, true> : append_kernel<128, 8, false>;
 }
 
 struct GatherParams {
