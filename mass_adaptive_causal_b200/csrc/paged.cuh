@@ -241,8 +241,10 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
   const int h0 = blockIdx.z * p.heads, nh = min(p.heads, p.pool.Hkv - h0);
   const int id = page_of(p.pool, b, slot);  // no page: its rows are left out, q is rotated all the same
 
-  // the units: K of every head, V of every head, Q
-  const int total = nh * (2 + p.G);
+  // the units: K of every head, V of every head, Q. With the angles in a table Q is not cut into
+  // units but walked along the tokens, all heads of one side by side, as it lies in memory.
+  const int nq = nh * p.G;
+  const int total = 2 * nh + (TABLE ? 0 : nq);
   const __nv_bfloat16* src = nullptr;
   long long stride = 0;
   auto aim = [&](int u) {
@@ -265,9 +267,42 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
       raw[ps][1] = *reinterpret_cast<const uint4*>(src + r * stride + ch.c1);
     }
   };
+  // Q's rows and heads, the next to be loaded (lq) and to be stored (sq)
+  struct At {
+    int row, head;
+  } lq = {0, 0}, sq;
+  if (TABLE && nq > 0) {
+    lq.row = (tid >> 3) / nq;
+    lq.head = (tid >> 3) - lq.row * nq;
+  } else {
+    lq.row = n;  // none
+  }
+  sq = lq;
+  const int q_rows = nq > 0 ? (APPEND_NT / 8) / nq : 0, q_heads = APPEND_NT / 8 - q_rows * nq;
+  auto step = [&](At& a) {
+    a.row += q_rows;
+    a.head += q_heads;
+    if (a.head >= nq) {
+      a.head -= nq;
+      ++a.row;
+    }
+  };
+  auto load_q = [&](int ps) {
+    if (lq.row >= n) return;
+    const __nv_bfloat16* at = p.q + (tok0 + lq.row) * p.q_tok +
+                              ((long long)h0 * p.G + lq.head) * p.q_head;
+    raw[ps][0] = *reinterpret_cast<const uint4*>(at + ch.c0);
+    raw[ps][1] = *reinterpret_cast<const uint4*>(at + ch.c1);
+    step(lq);
+  };
   aim(tid / LPU);
 #pragma unroll
-  for (int ps = 0; ps < PASSES; ++ps) load(ps, tid / LPU < total);
+  for (int ps = 0; ps < PASSES; ++ps) {
+    if (tid / LPU < total)
+      load(ps, true);
+    else if (TABLE)
+      load_q(ps);
+  }
 
   if (TABLE && p.rot > 0) {
     const int quarter = p.rot >> 2;
@@ -294,15 +329,30 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
     }
   }
   // a row's values in float32, rotated
-  auto values = [&](int ps, bool rotates, float (&x)[16]) {
+  auto values = [&](int ps, int r, bool rotates, float (&x)[16]) {
     unpack8(raw[ps][0], x);
     unpack8(raw[ps][1], x + 8);
     if (!rotates) return;
     float4 cs[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      cs[j] = TABLE ? table[(r0 + STEP * ps) * 32 + j * 8 + t] : own[TABLE ? 0 : ps][j];
+      cs[j] = TABLE ? table[r * 32 + j * 8 + t] : own[TABLE ? 0 : ps][j];
     rotate<INTERLEAVED>(x, cs);
+  };
+  auto store_q = [&](int ps, int r, __nv_bfloat16* dst) {
+    uint4 w[2] = {raw[ps][0], raw[ps][1]};  // not rotated: bit for bit
+    if (ch.freq >= 0) {
+      float x[16];
+      values(ps, r, true, x);
+      uint32_t* z = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        z[i] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + ch.c0) = w[0];
+    *reinterpret_cast<uint4*>(dst + ch.c1) = w[1];
   };
 
   for (int u0 = 0; u0 < total; u0 += UNITS) {
@@ -326,7 +376,7 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
           for (int ps = 0; ps < PASSES; ++ps) {
             if (r0 + STEP * ps >= n) continue;
             float x[16];
-            values(ps, rotates, x);
+            values(ps, r0 + STEP * ps, rotates, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i)  // a NaN is passed over
               m = fmaxf(m, finite && fabsf(x[i]) == inf ? 0.f : fabsf(x[i]));
@@ -386,7 +436,7 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
           const int r = r0 + STEP * ps;
           if (r < n && id >= 0) {
             float x[16];
-            values(ps, rotates, x);
+            values(ps, r, rotates, x);
             if (infinite)  // e4m3 has none
 #pragma unroll
               for (int i = 0; i < 16; ++i)
@@ -400,34 +450,34 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
             *reinterpret_cast<uint2*>(row + ch.c0) = make_uint2(w[0], w[1]);
             *reinterpret_cast<uint2*>(row + ch.c1) = make_uint2(w[2], w[3]);
           }
-          load(ps, more);
+          if (TABLE && !more)
+            load_q(ps);
+          else
+            load(ps, more);
         }
       }
     }
-    if (!kv && u < total) {
+    if (!TABLE && !kv && u < total) {
       __nv_bfloat16* dst = p.q_out + ((long long)h0 * p.G + (u - 2 * nh)) * p.qo_head + tok0 * p.qo_tok;
 #pragma unroll
       for (int ps = 0; ps < PASSES; ++ps) {
         const int r = r0 + STEP * ps;
-        if (r < n) {
-          uint4 w[2] = {raw[ps][0], raw[ps][1]};  // not rotated: bit for bit
-          if (rotates) {
-            float x[16];
-            values(ps, true, x);
-            uint32_t* z = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-              z[i] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-          }
-          *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c0) = w[0];
-          *reinterpret_cast<uint4*>(dst + r * p.qo_tok + ch.c1) = w[1];
-        }
+        if (r < n) store_q(ps, r, dst + r * p.qo_tok);
         load(ps, more);
       }
     }
   }
+  if (TABLE)
+    while (sq.row < n) {
+#pragma unroll
+      for (int ps = 0; ps < PASSES; ++ps) {
+        if (sq.row >= n) break;
+        store_q(ps, sq.row, p.q_out + (tok0 + sq.row) * p.qo_tok +
+                                ((long long)h0 * p.G + sq.head) * p.qo_head);
+        step(sq);
+        load_q(ps);
+      }
+    }
 }
 
 using AppendKernel = void (*)(AppendParams);
