@@ -60,6 +60,7 @@ constexpr uint32_t RING = NST * TILE_BYTES;
 constexpr int MAXC = 16;              // blocks of a cluster
 constexpr int NMETA = 16;             // tiles whose scales are held
 constexpr int TERMS = 4;
+constexpr int SBUF = 4;                // buffers of scores in tensor memory
 
 struct Params {
   Pool pool;
@@ -95,25 +96,46 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, ui
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
          (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46;
 }
+// N consecutive columns of this thread's TMEM lane: tmem_ld starts the load, and tmem_ready
+// (after tmem_wait, which waits for all that were started) hands its registers over.
 template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
   static_assert(N == 16 || N == 32, "");
   if constexpr (N == 32) {
-    sm100::tmem_ld32(taddr, v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
   } else {
-    uint32_t r[16];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
   }
+}
+__device__ __forceinline__ void tmem_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_ready(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 16)
+    asm volatile(""
+                 : "+r"(r[e]), "+r"(r[e + 1]), "+r"(r[e + 2]), "+r"(r[e + 3]), "+r"(r[e + 4]),
+                   "+r"(r[e + 5]), "+r"(r[e + 6]), "+r"(r[e + 7]), "+r"(r[e + 8]), "+r"(r[e + 9]),
+                   "+r"(r[e + 10]), "+r"(r[e + 11]), "+r"(r[e + 12]), "+r"(r[e + 13]),
+                   "+r"(r[e + 14]), "+r"(r[e + 15]));
 }
 // The largest of a warp's values, in every lane; a NaN is passed over.
 __device__ __forceinline__ float warp_max(float x) {
@@ -179,9 +201,9 @@ struct Shared {
   unsigned char p[2][T * TERMS * GH];  // P of a tile: key k's terms in rows of sixteen bytes
   unsigned char q[TERMS * GH * D];     // q's terms [term][head][128], 128-byte swizzle
   Meta meta[NMETA];
-  float2 part[2][4][GH];               // a tile's statistics by warp
+  float2 part[2][SBUF][4][GH];         // tiles' statistics by warp
   uint64_t full[NST], empty[NST];
-  uint64_t s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t s_full[SBUF], s_empty[SBUF], p_full[2], o_full[2], o_empty[2];
   float undo[GMAX];                    // what a head's products are multiplied with
   float mfin[GMAX], lfin[GMAX];        // final max (log2 units) and mass
   float bound[GMAX];
@@ -250,11 +272,13 @@ __device__ __forceinline__ void split_q(const uint4& raw, Shared<GH>& sh, float 
 
 // The four terms' columns of a row joined, per head.
 template <int GH>
-__device__ __forceinline__ void join_terms(const float (&v)[TERMS * GH], float (&x)[GH]) {
+__device__ __forceinline__ void join_terms(const uint32_t (&v)[TERMS * GH], float (&x)[GH]) {
 #pragma unroll
-  for (int g = 0; g < GH; ++g)
-    x[g] = fmaf(fmaf(fmaf(v[3 * GH + g], 1.f / 16.f, v[2 * GH + g]), 1.f / 16.f, v[GH + g]),
-                1.f / 16.f, v[g]);
+  for (int g = 0; g < GH; ++g) {
+    x[g] = __uint_as_float(v[3 * GH + g]);
+#pragma unroll
+    for (int k = 2; k >= 0; --k) x[g] = fmaf(x[g], 1.f / 16.f, __uint_as_float(v[k * GH + g]));
+  }
 }
 
 // A key's probabilities (scaled by 2^8) as e4m3 terms into its row of P.
@@ -326,7 +350,7 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
         if (lane == 0 && turn > 0)
           ok = mbar_wait(smem_u32(&sh.empty[st]), (turn - 1) & 1, abort, 0x511);
         if (!__shfl_sync(0xffffffffu, (int)ok, 0)) return false;
-        if (mine && w == 0) {  // sixteen tiles are held, the softmax is eight behind at most
+        if (mine && w == 0) {  // sixteen tiles are held, the softmax is ten behind at most
           Meta& m = sh.meta[(meta0 + (uint32_t)(i0 + j)) % NMETA];
           if (sub == 0) {
             m.pos = pos;
@@ -349,46 +373,73 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
   return true;
 }
 
-// One thread issues the products. S of the tile in ring stage `seq` into S buffer s & 1:
+// The warp that issues the products runs as one, so that descriptors and addresses stay in uniform
+// registers, and elects a lane for each group of instructions (a single thread's loop took 420
+// cycles to issue a tile's, which bounded a block's rate).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+struct Issuer {
+  uint64_t k, v, q, p;  // descriptors of ring stage 0 as keys and as values, of q and of P
+  uint32_t tmem;
+};
+// S of the tile in ring stage `seq` into S buffer s % SBUF:
 template <int GH>
-__device__ __forceinline__ bool issue_s(Shared<GH>& sh, unsigned char* ring, uint32_t seq,
-                                        uint32_t s) {
+__device__ __forceinline__ bool issue_s(Shared<GH>& sh, const Issuer& is, uint32_t seq, uint32_t s) {
   constexpr uint32_t ID = idesc_e4m3(T, TERMS * GH, false, false);
   volatile int* abort = &sh.abort;
-  const uint32_t st = seq % NST, buf = s & 1;
-  if (!mbar_wait(smem_u32(&sh.full[st]), (seq / NST) & 1, abort, 0x512)) return false;
-  if (s >= 2 && !mbar_wait(smem_u32(&sh.s_empty[buf]), ((s >> 1) - 1) & 1, abort, 0x513))
-    return false;
+  const uint32_t st = seq % NST, buf = s % SBUF;
+  bool ok = mbar_wait(smem_u32(&sh.full[st]), (seq / NST) & 1, abort, 0x512);
+  if (s >= SBUF) ok = ok && mbar_wait(smem_u32(&sh.s_empty[buf]), (s / SBUF - 1) & 1, abort, 0x513);
+  if (!__all_sync(0xffffffffu, ok)) return false;
   sm100::tc_fence_after();
-  const uint64_t a = sm100::sdesc_sw128(smem_u32(ring) + st * TILE_BYTES, 16, 1024);
-  const uint64_t b = sm100::sdesc_sw128(smem_u32(sh.q), 16, 1024);
+  if (elect_one()) {
+    const uint64_t a = is.k + st * (TILE_BYTES >> 4);
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk)
-    mma_e4m3(sh.tmem + buf * (TERMS * GH), a + 2 * kk, b + 2 * kk, ID, kk > 0);
-  sm100::mma_commit(smem_u32(&sh.empty[st]));
-  sm100::mma_commit(smem_u32(&sh.s_full[buf]));
+    for (int kk = 0; kk < 4; ++kk)
+      mma_e4m3(is.tmem + buf * (TERMS * GH), a + 2 * kk, is.q + 2 * kk, ID, kk > 0);
+    sm100::mma_commit(smem_u32(&sh.s_full[buf]));
+    sm100::mma_commit(smem_u32(&sh.empty[st]));
+  }
+  __syncwarp();
   return true;
 }
 // O of the i-th tile with values, V in ring stage `seq`:
 template <int GH>
-__device__ __forceinline__ bool issue_o(Shared<GH>& sh, unsigned char* ring, uint32_t seq,
-                                        uint32_t i) {
+__device__ __forceinline__ bool issue_o(Shared<GH>& sh, const Issuer& is, uint32_t seq, uint32_t i) {
   constexpr uint32_t ID = idesc_e4m3(T, TERMS * GH, true, true);
   volatile int* abort = &sh.abort;
   const uint32_t st = seq % NST, buf = i & 1;
-  if (!mbar_wait(smem_u32(&sh.p_full[buf]), (i >> 1) & 1, abort, 0x514)) return false;
-  if (!mbar_wait(smem_u32(&sh.full[st]), (seq / NST) & 1, abort, 0x515)) return false;
-  if (i >= 2 && !mbar_wait(smem_u32(&sh.o_empty[buf]), ((i >> 1) - 1) & 1, abort, 0x516))
-    return false;
+  bool ok = mbar_wait(smem_u32(&sh.p_full[buf]), (i >> 1) & 1, abort, 0x514);
+  ok = ok && mbar_wait(smem_u32(&sh.full[st]), (seq / NST) & 1, abort, 0x515);
+  if (i >= 2) ok = ok && mbar_wait(smem_u32(&sh.o_empty[buf]), ((i >> 1) - 1) & 1, abort, 0x516);
+  if (!__all_sync(0xffffffffu, ok)) return false;
   sm100::tc_fence_after();
-  const uint64_t a = sm100::sdesc_sw128(smem_u32(ring) + st * TILE_BYTES, TILE_BYTES, 1024);
-  const uint64_t b = sdesc_plain(smem_u32(sh.p[buf]), 128, T * 16);
+  if (elect_one()) {
+    const uint64_t a = is.v + st * (TILE_BYTES >> 4), b = is.p + buf * (T * TERMS * GH >> 4);
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4 KB of V, 512 bytes of P
-    mma_e4m3(sh.tmem + (2 + buf) * (TERMS * GH), a + 256 * kk, b + 32 * kk, ID, kk > 0);
-  sm100::mma_commit(smem_u32(&sh.empty[st]));
-  sm100::mma_commit(smem_u32(&sh.o_full[buf]));
+    for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4 KB of V, 512 bytes of P
+      mma_e4m3(is.tmem + (SBUF + buf) * (TERMS * GH), a + 256 * kk, b + 32 * kk, ID, kk > 0);
+    sm100::mma_commit(smem_u32(&sh.o_full[buf]));
+    sm100::mma_commit(smem_u32(&sh.empty[st]));
+  }
+  __syncwarp();
   return true;
+}
+// Scores two tiles ahead of the values.
+template <int GH>
+__device__ __forceinline__ bool issue_pairs(Shared<GH>& sh, const Issuer& is, int tiles, uint32_t seq0,
+                                            uint32_t s0) {
+  bool ok = true;
+  for (int i = 0; i < 2 && i < tiles && ok; ++i) ok = issue_s<GH>(sh, is, seq0 + 2 * i, s0 + i);
+  for (int i = 0; i < tiles && ok; ++i) {
+    ok = issue_o<GH>(sh, is, seq0 + 2 * i + 1, i);
+    if (ok && i + 2 < tiles) ok = issue_s<GH>(sh, is, seq0 + 2 * (i + 2), s0 + i + 2);
+  }
+  return ok;
 }
 
 // A softmax warp's wait. When it runs out the warp goes on all the same, over whatever lies
@@ -406,23 +457,21 @@ __device__ __forceinline__ void release(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
 }
 
-// Scores of this thread's key in log2 units, -inf behind the sequence; S buffer s & 1 (whose
-// barrier the caller waited for) is given back. What the caller wants of m is read before: the
-// load warp may overwrite it later.
+// Scores of this thread's key in log2 units, -inf behind the sequence, of the tile whose
+// products `v` holds.
 template <int GH>
-__device__ __forceinline__ void scores(Shared<GH>& sh, uint32_t s, const Meta& m, int len,
+__device__ __forceinline__ void scores(const uint32_t (&v)[TERMS * GH], float ks, int left,
                                        const float (&undo)[GH], float (&x)[GH]) {
-  const int key = threadIdx.x;
-  const uint32_t buf = s & 1;
-  sm100::tc_fence_after();
-  float v[TERMS * GH];
-  tmem_ld(sh.tmem + buf * (TERMS * GH) + ((uint32_t)(key >> 5) << 21), v);
-  const float ks = m.k[key >> 4];
-  const bool in = key < len - m.pos;
-  release(&sh.s_empty[buf]);
   join_terms<GH>(v, x);
 #pragma unroll
-  for (int g = 0; g < GH; ++g) x[g] = in ? x[g] * (undo[g] * ks) : kNegInf;
+  for (int g = 0; g < GH; ++g) x[g] = (int)threadIdx.x < left ? x[g] * (undo[g] * ks) : kNegInf;
+}
+// The S-th tile's products, when they are there.
+template <int GH>
+__device__ __forceinline__ void start_scores(Shared<GH>& sh, uint32_t s, uint32_t (&v)[TERMS * GH]) {
+  warp_wait(&sh.s_full[s % SBUF], (s / SBUF) & 1, &sh.abort, 0x517);
+  sm100::tc_fence_after();
+  tmem_ld(sh.tmem + (s % SBUF) * (TERMS * GH) + ((threadIdx.x >> 5) << 21), v);
 }
 
 // out += O of the i-th tile, f[g] times, for the heads that keep it (a value that is NaN
@@ -433,8 +482,10 @@ __device__ __forceinline__ void add_o(Shared<GH>& sh, uint32_t i, const float (&
   const uint32_t buf = i & 1;
   warp_wait(&sh.o_full[buf], (i >> 1) & 1, &sh.abort, 0x518);
   sm100::tc_fence_after();
-  float v[TERMS * GH];
-  tmem_ld(sh.tmem + (2 + buf) * (TERMS * GH) + ((threadIdx.x >> 5) << 21), v);
+  uint32_t v[TERMS * GH];
+  tmem_ld(sh.tmem + (SBUF + buf) * (TERMS * GH) + ((threadIdx.x >> 5) << 21), v);
+  tmem_wait();
+  tmem_ready(v);
   release(&sh.o_empty[buf]);
   float x[GH];
   join_terms<GH>(v, x);
@@ -457,7 +508,11 @@ __device__ __forceinline__ void softmax_pv(Shared<GH>& sh, unsigned char* ring, 
   for (int i = 0; i < tiles; ++i) {
     const Meta& m = sh.meta[(s0 + (uint32_t)i) % NMETA];
     const uint32_t s = s0 + (uint32_t)i;
-    warp_wait(&sh.s_full[s & 1], (s >> 1) & 1, &sh.abort, 0x517);
+    uint32_t raw[TERMS * GH];
+    start_scores<GH>(sh, s, raw);
+    // what is wanted of m is read before the products' buffer is given back: the load warp may
+    // overwrite it later
+    const float ks = m.k[key >> 4];
     const int left = len - m.pos;
     const uint32_t heads = FIXED ? m.heads : 0xffu;
     // pages of different scales: V's bytes count u, the largest, and P takes the rest
@@ -468,7 +523,10 @@ __device__ __forceinline__ void softmax_pv(Shared<GH>& sh, unsigned char* ring, 
                           fmaxf(fmaxf(fabsf(v1.x), fabsf(v1.y)), fmaxf(fabsf(v1.z), fabsf(v1.w))));
     const float ratio = vs == u ? 1.f : (vs == 0.f ? 0.f : vs / u);
     float x[GH];
-    scores<GH>(sh, s, m, len, undo, x);
+    tmem_wait();
+    tmem_ready(raw);
+    release(&sh.s_empty[s % SBUF]);
+    scores<GH>(raw, ks, left, undo, x);
     if (!FIXED) {
       bool above = false;
 #pragma unroll
@@ -804,7 +862,8 @@ template <int GH, bool RULE>
 __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ CUtensorMap tmK,
                                                        const __grid_constant__ CUtensorMap tmV,
                                                        const Params p) {
-  constexpr int NCOL = TERMS * GH;
+  constexpr uint32_t TCOLS = 8 * TERMS * GH;  // SBUF buffers of S and two of O; a power of two
+  static_assert(SBUF + 2 <= 8 && 2 * TCOLS <= 512, "two blocks share an SM's tensor memory");
   extern __shared__ unsigned char smem[];
   Shared<GH>& sh = *reinterpret_cast<Shared<GH>*>(smem + RING);
   if (smem_u32(smem) & 1023u) {  // the swizzle needs it; without static shared memory it holds
@@ -829,10 +888,12 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
         sm100::mbar_init(smem_u32(&sh.full[s]), 1);
         sm100::mbar_init(smem_u32(&sh.empty[s]), 1);
       }
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < SBUF; ++s) {
         sm100::mbar_init(smem_u32(&sh.s_full[s]), 1);
-        sm100::mbar_init(smem_u32(&sh.o_full[s]), 1);
         sm100::mbar_init(smem_u32(&sh.s_empty[s]), 4);
+      }
+      for (int s = 0; s < 2; ++s) {
+        sm100::mbar_init(smem_u32(&sh.o_full[s]), 1);
         sm100::mbar_init(smem_u32(&sh.o_empty[s]), 4);
         sm100::mbar_init(smem_u32(&sh.p_full[s]), 4);
       }
@@ -866,7 +927,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
   }
   if (warp != W_LOAD) {  // the load warp needs none of this
     if (warp == W_TMEM) {
-      sm100::tmem_alloc(smem_u32(&sh.tmem), 4 * NCOL);
+      sm100::tmem_alloc(smem_u32(&sh.tmem), TCOLS);
       sm100::tmem_relinquish();
     } else if (warp < 4) {
       split_q<GH>(qraw, sh, p.scale_log2);
@@ -879,54 +940,87 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
 #pragma unroll
     for (int g = 0; g < GH; ++g) undo[g] = sh.undo[g];
   }
+  Issuer issuer;
+  issuer.k = sm100::sdesc_sw128(smem_u32(smem), 16, 1024);
+  issuer.v = sm100::sdesc_sw128(smem_u32(smem), TILE_BYTES, 1024);
+  issuer.q = sm100::sdesc_sw128(smem_u32(sh.q), 16, 1024);
+  issuer.p = sdesc_plain(smem_u32(sh.p), 128, T * 16);
+  issuer.tmem = warp == W_MMA ? __shfl_sync(0xffffffffu, sh.tmem, 0) : 0u;
 
   if constexpr (RULE) {
     // ---- A: statistics
     if (warp == W_LOAD) {
       ok = load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, false, 0u, 0u, own_tile);
     } else if (warp == W_MMA) {
-      if (lane == 0)
-        for (int i = 0; i < tiles && ok; ++i) ok = issue_s<GH>(sh, smem, i, i);
+      for (int i = 0; i < tiles && ok; ++i) ok = issue_s<GH>(sh, issuer, i, i);
     } else if (warp < 4) {
-      for (int i = 0; i < tiles; ++i) {
-        float x[GH];
-        warp_wait(&sh.s_full[i & 1], (i >> 1) & 1, &sh.abort, 0x517);
-        scores<GH>(sh, i, sh.meta[i % NMETA], len, undo, x);
-        // a warp's 32 keys; a quarter without a finite score: mass 0
-        float m[GH];
+      // NB tiles at a time: their loads and reductions overlap
+      constexpr int NB = GH == 4 ? 4 : 2;
+      for (int i = 0; i < tiles; i += NB) {
+        uint32_t raw[NB][TERMS * GH];
+        float ks[NB] = {};
+        int left[NB] = {};
 #pragma unroll
-        for (int g = 0; g < GH; ++g) {
-          m[g] = warp_max(x[g]);
-          x[g] = ex2_approx(x[g] - (m[g] == kNegInf ? 0.f : m[g]));
+        for (int q = 0; q < NB; ++q) {
+          if (i + q >= tiles) break;
+          start_scores<GH>(sh, i + q, raw[q]);
+          const Meta& m = sh.meta[(i + q) % NMETA];
+          ks[q] = m.k[tid >> 4];
+          left[q] = len - m.pos;
+        }
+        tmem_wait();
+#pragma unroll
+        for (int q = 0; q < NB; ++q) {
+          tmem_ready(raw[q]);
+          if (i + q < tiles) release(&sh.s_empty[(i + q) % SBUF]);
+        }
+        float x[NB][GH], m[NB][GH];
+#pragma unroll
+        for (int q = 0; q < NB; ++q) {
+          scores<GH>(raw[q], ks[q], left[q], undo, x[q]);
+          // a warp's 32 keys; a quarter without a finite score: mass 0
+#pragma unroll
+          for (int g = 0; g < GH; ++g) {
+            m[q][g] = warp_max(x[q][g]);
+            x[q][g] = ex2_approx(x[q][g] - (m[q][g] == kNegInf ? 0.f : m[q][g]));
+          }
         }
         // sums: each step halves the heads a lane is at work on, lane / (32 / GH) is left with one
 #pragma unroll
-        for (int n = GH / 2, d = 16; n >= 1; n >>= 1, d >>= 1)
+        for (int n = GH / 2, d = 16; n >= 1; n >>= 1, d >>= 1) {
+          const bool up = lane & d;
 #pragma unroll
-          for (int g = 0; g < n; ++g) {
-            const bool up = lane & d;
-            const float give = up ? x[g] : x[g + n], keep_ = up ? x[g + n] : x[g];
-            x[g] = keep_ + __shfl_xor_sync(0xffffffffu, give, d);
-            const float mk = up ? m[g + n] : m[g];
-            m[g] = mk;
-          }
+          for (int g = 0; g < n; ++g)
 #pragma unroll
-        for (int d = 16 / GH; d >= 1; d >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
-        const int g = lane / (32 / GH);
-        if (lane % (32 / GH) == 0) sh.part[i & 1][warp][g] = make_float2(m[0], x[0]);
+            for (int q = 0; q < NB; ++q) {
+              const float give = up ? x[q][g] : x[q][g + n];
+              x[q][g] = (up ? x[q][g + n] : x[q][g]) + __shfl_xor_sync(0xffffffffu, give, d);
+              m[q][g] = up ? m[q][g + n] : m[q][g];
+            }
+        }
+#pragma unroll
+        for (int d = 16 / GH; d >= 1; d >>= 1)
+#pragma unroll
+          for (int q = 0; q < NB; ++q) x[q][0] += __shfl_xor_sync(0xffffffffu, x[q][0], d);
+        auto& part = sh.part[(i / NB) & 1];
+        if (lane % (32 / GH) == 0)
+#pragma unroll
+          for (int q = 0; q < NB; ++q)
+            part[q][warp][lane / (32 / GH)] = make_float2(m[q][0], x[q][0]);
         sync_softmax();
-        if (warp == (i & 3) && lane < G) {  // the four quarters' statistics as the tile's
-          float2 q[4];
+        if (warp < NB && i + warp < tiles && lane < G) {  // the four quarters' statistics as the tile's
+          float2 y[4];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) q[w] = sh.part[i & 1][w][lane];
-          float top = fmaxf(fmaxf(q[0].x, q[1].x), fmaxf(q[2].x, q[3].x));
+          for (int w = 0; w < 4; ++w) y[w] = part[warp][w][lane];
+          float top = fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x));
           const float z = top == kNegInf ? 0.f : top;
           float sum = 0.f;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) sum += q[w].y * ex2_approx(q[w].x - z);
+          for (int w = 0; w < 4; ++w) sum += y[w].y * ex2_approx(y[w].x - z);
           if (isnan(sum)) top = sum;  // a tile with a NaN score is kept, and shows
-          stats[i * p.GP + lane] = make_float2(top, sum);
+          stats[(i + warp) * p.GP + lane] = make_float2(top, sum);
         }
+        __syncwarp();
       }
     }
     if (sh.abort) sm100::drain_in_flight();
@@ -952,13 +1046,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
       };
       if (ok) load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, items, true, done, done, kept_tile);
     } else if (warp == W_MMA) {
-      if (lane == 0) {
-        for (int i = 0; i < 2 && i < items && ok; ++i) ok = issue_s<GH>(sh, smem, done + 2 * i, done + i);
-        for (int i = 0; i < items && ok; ++i) {
-          ok = issue_o<GH>(sh, smem, done + 2 * i + 1, i);
-          if (ok && i + 2 < items) ok = issue_s<GH>(sh, smem, done + 2 * (i + 2), done + i + 2);
-        }
-      }
+      if (ok) issue_pairs<GH>(sh, issuer, items, done, done);
     } else if (warp < 4) {
 #pragma unroll
       for (int g = 0; g < GH; ++g) mref[g] = g < G ? sh.mfin[g] : 0.f;
@@ -968,13 +1056,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     if (warp == W_LOAD) {
       ok = load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, true, 0u, 0u, own_tile);
     } else if (warp == W_MMA) {
-      if (lane == 0) {
-        for (int i = 0; i < 2 && i < tiles && ok; ++i) ok = issue_s<GH>(sh, smem, 2 * i, i);
-        for (int i = 0; i < tiles && ok; ++i) {
-          ok = issue_o<GH>(sh, smem, 2 * i + 1, i);
-          if (ok && i + 2 < tiles) ok = issue_s<GH>(sh, smem, 2 * (i + 2), i + 2);
-        }
-      }
+      issue_pairs<GH>(sh, issuer, tiles, 0u, 0u);
     } else if (warp < 4) {
       softmax_pv<GH, false>(sh, smem, len, tiles, 0u, 0u, undo, mref, l, out);
       // the block's mass per head: every thread has its own keys'
@@ -1001,7 +1083,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
   // be, and a deallocation by part of a warp never ends)
   if (warp == W_TMEM) {
     sm100::tc_fence_after();
-    sm100::tmem_dealloc(sh.tmem, 4 * NCOL);
+    sm100::tmem_dealloc(sh.tmem, TCOLS);
   }
   if (!RULE && C > 1) cluster_wait();  // the other blocks run
   join_and_store<GH>(p, sh, out, rank, o, !RULE);
