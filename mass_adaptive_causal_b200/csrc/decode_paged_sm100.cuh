@@ -382,6 +382,13 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(p));
   return p != 0;
 }
+// Waits for two barriers; what is mostly there already costs one look at both.
+__device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                          uint32_t parity1, volatile int* abort, unsigned where) {
+  const bool ok0 = sm100::mbar_try_wait(bar0, parity0), ok1 = sm100::mbar_try_wait(bar1, parity1);
+  return (ok0 || mbar_wait(bar0, parity0, abort, where)) &&
+         (ok1 || mbar_wait(bar1, parity1, abort, where));
+}
 struct Issuer {
   uint64_t k, v, q, p;  // descriptors of ring stage 0 as keys and as values, of q and of P
   uint32_t tmem;
@@ -392,8 +399,9 @@ __device__ __forceinline__ bool issue_s(Shared<GH>& sh, const Issuer& is, uint32
   constexpr uint32_t ID = idesc_e4m3(T, TERMS * GH, false, false);
   volatile int* abort = &sh.abort;
   const uint32_t st = seq % NST, buf = s % SBUF;
-  bool ok = mbar_wait(smem_u32(&sh.full[st]), (seq / NST) & 1, abort, 0x512);
-  if (s >= SBUF) ok = ok && mbar_wait(smem_u32(&sh.s_empty[buf]), (s / SBUF - 1) & 1, abort, 0x513);
+  // a barrier that nothing has used yet counts as through with the phase before its first
+  const bool ok = wait_both(smem_u32(&sh.full[st]), (seq / NST) & 1, smem_u32(&sh.s_empty[buf]),
+                            (s / SBUF + 1) & 1, abort, 0x512);
   if (!__all_sync(0xffffffffu, ok)) return false;
   sm100::tc_fence_after();
   if (elect_one()) {
@@ -413,9 +421,9 @@ __device__ __forceinline__ bool issue_o(Shared<GH>& sh, const Issuer& is, uint32
   constexpr uint32_t ID = idesc_e4m3(T, TERMS * GH, true, true);
   volatile int* abort = &sh.abort;
   const uint32_t st = seq % NST, buf = i & 1;
-  bool ok = mbar_wait(smem_u32(&sh.p_full[buf]), (i >> 1) & 1, abort, 0x514);
-  ok = ok && mbar_wait(smem_u32(&sh.full[st]), (seq / NST) & 1, abort, 0x515);
-  if (i >= 2) ok = ok && mbar_wait(smem_u32(&sh.o_empty[buf]), ((i >> 1) - 1) & 1, abort, 0x516);
+  bool ok = wait_both(smem_u32(&sh.full[st]), (seq / NST) & 1, smem_u32(&sh.o_empty[buf]),
+                      ((i >> 1) + 1) & 1, abort, 0x515);
+  ok = ok && mbar_wait(smem_u32(&sh.p_full[buf]), (i >> 1) & 1, abort, 0x514);
   if (!__all_sync(0xffffffffu, ok)) return false;
   sm100::tc_fence_after();
   if (elect_one()) {
@@ -763,7 +771,7 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
       if (p.per_head ? lane == 0 : lane < G) sh.bound[p.per_head ? warp : lane] = w.bound;
     }
     __syncwarp();
-    __syncthreads();
+    if (last > first) __syncthreads();
     for (int wi = first + warp; wi < last; wi += NT / 32) {
       const float2* at = loc + (size_t)(wi * 32 + lane - lo) * GP;
       bool may = false;
@@ -781,7 +789,7 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
       if (!p.per_head && lane == 0) keep[wi] = open;
     }
     __syncwarp();
-    __syncthreads();
+    if (last > first) __syncthreads();
     if (walks)
       for (int w0 = last - 1; w0 >= first; w0 -= 32) {  // 32 words at a time, a lane each
         const uint32_t mine = w0 - lane >= first ? keep[unit * words + w0 - lane] : 0u;
@@ -810,32 +818,22 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
       uint32_t any = 0;
       if (w0 + lane < live)
         for (int u = 0; u < units; ++u) any |= keep[u * words + w0 + lane];
-      int at = __popc(any);
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, at, d);
-        if (lane >= d) at += y;
-      }
-      const int total = __shfl_sync(0xffffffffu, at, 31);
-      at += count - __popc(any);
-      int mine = at >> p.C_log2, turn = at & (C - 1);
-      while (any) {
-        const int bit = __ffs(any) - 1;
-        any &= any - 1;
-        if (turn == (int)rank) {
+      uint32_t some = __ballot_sync(0xffffffffu, any != 0u);
+      while (some) {  // a word with kept tiles, a lane each
+        const int src = __ffs(some) - 1, wi = w0 + src;
+        some &= some - 1;
+        const uint32_t word = __shfl_sync(0xffffffffu, any, src);
+        const int n = count + __popc(word & ((1u << lane) - 1u));
+        if (((word >> lane) & 1u) && (n & (C - 1)) == (int)rank) {
           uint32_t heads = 0xffu;
           if (p.per_head) {
             heads = 0;
-            for (int u = 0; u < units; ++u) heads |= ((keep[u * words + w0 + lane] >> bit) & 1u) << u;
+            for (int u = 0; u < units; ++u) heads |= ((keep[u * words + wi] >> lane) & 1u) << u;
           }
-          list[mine] = (uint32_t)((w0 + lane) * 32 + bit) | heads << 24;
+          list[n >> p.C_log2] = (uint32_t)(wi * 32 + lane) | heads << 24;
         }
-        if (++turn == C) {
-          turn = 0;
-          ++mine;
-        }
+        count += __popc(word);
       }
-      count += total;
     }
     if (lane == 0) sh.items = (count - (int)rank + C - 1) >> p.C_log2;
   } else if (rank == 0) {
