@@ -274,7 +274,7 @@ mala_status mala_decode_noalloc(const void* q, const void* Kcache,
  * sequence b is row p % page_size of page page_table[b][p / page_size]. A
  * page may stand in the tables of several sequences (a shared prefix); a page
  * that a mala_cache_append writes to belongs to one sequence. Table entries past a
- * sequence's last page are not read.
+ * sequence's last page may hold anything.
  *
  * All pointers are device pointers: the pools 16-byte aligned, the rest by
  * their element. The strides are in bytes (the elements are bytes), positive
@@ -359,9 +359,13 @@ mala_status mala_cache_append(const mala_paged_cache* cache, const void* k,
  * Trace   kept_tiles: [batch][Hkv]; keep_bits: [batch][Hkv][ceil(nt/32)], nt =
  *         ceil(max_seqlen / 128); with per_head = 1, [batch][Hq] and
  *         [batch][Hq][ceil(nt/32)].
+ * Precision: q and the probabilities enter the e4m3 products as four e4m3 terms
+ * each. A probability is rounded to f16, and below that to 2^-30 of the row's
+ * largest; where a 128-key tile has pages of different value scales, both count
+ * relative to the largest of them. Sums, maxima and masses are float32.
  * No workspace. Supported: 1 <= Hq / Hkv <= 8, batch, Hkv <= 65535;
- * MALA_ERR_TOO_LARGE when the statistics of max_seqlen do not fit in shared
- * memory.
+ * MALA_ERR_TOO_LARGE when the statistics of max_seqlen do not fit in the shared
+ * memory of a cluster of 16 blocks (above 2.9 million tokens at Hq / Hkv = 8).
  */
 mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q,
                               void* o, const int32_t* seq_lens, int batch,

@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
   }
   const int start = len - count;
   const int slot = (start >> p.pool.page_log2) + blockIdx.x;
+  if ((long long)slot << p.pool.page_log2 >= len) return;
   const int begin = max(start, slot << p.pool.page_log2);
   const int end = (int)min((long long)len, (long long)(slot + 1) << p.pool.page_log2);
-  if (begin >= end) return;
   const int row0 = begin - (slot << p.pool.page_log2), n = end - begin;
   const long long tok0 = (long long)first + (begin - start);
   const int tid = threadIdx.x, t = tid & 7, r0 = (tid % LPU) >> 3;

@@ -12,12 +12,15 @@ e4m3 2^-4):
       with the largest value scaled to at least 2^7: 2^-29 max|q| an element. Then the score is scaled
       (three roundings) and, like the row's reference, taken as a power of two: p is off by
       a relative 2 ((128 * 2^-23 + 4 * 2^-24) A + 2^-29 max|q| sum|k|) + 2^-21. P is rounded
-      to f16 for the product with V: 2^-11. It goes in as three e4m3 terms in the same
-      way, scaled to at most 2^8 with the largest p of its 32 keys at 2^8: what is left is at most 2^-10 /
-      2^8 / 2^8 = 2^-26 of that largest p. The sum l has the same error as p. Then the
-      output's rounding to bf16. With S = sum p |v|, U = sum over 32-key chunks of (largest p
-      of the chunk) * (sum |v| of the chunk):
-      |o - ref| <= 2^-8 |ref| + S (2^-11 + 4 (129 * 2^-23 A + 2^-29 max|q| sum|k|) + 2^-20) + 2^-26 U.
+      to f16 for the product with V: 2^-11. It goes in as four e4m3 terms in the same way, scaled
+      to 2^8 at a reference that is at most the row's largest p: what is left is at most
+      2^-10 / 2^12 / 2^8 = 2^-30 of that largest p, and f16's own smallest step, 2^-25 / 2^8, is
+      less. Where a tile's pages have different value scales, a key's P takes the ratio of its
+      scale to the tile's largest, u (one more rounding of 2^-24), and the rest counts against
+      u |v8| instead of |v| = scale |v8|. The sum l has the same error as p. Then the
+      output's rounding to bf16. With S = sum p |v|, U = (largest p) * sum u |v8| (tile by tile
+      its own u; sum |v| where the scales are one):
+      |o - ref| <= 2^-8 |ref| + S (2^-11 + 4 (129 * 2^-23 A + 2^-29 max|q| sum|k|) + 2^-20) + 2^-30 U.
 """
 
 from __future__ import annotations
@@ -167,6 +170,11 @@ class RefCache:
 
 def sequence(cache_tensors, table, b, n):
     """K, V [Hkv, n, 128] float64 of sequence b."""
+    return _sequence(cache_tensors, table, b, n)[:2]
+
+
+def _sequence(cache_tensors, table, b, n):
+    """K, V, and |v8| times the largest value scale of the key's 128-key tile."""
     k_pages, v_pages, k_scale, v_scale = cache_tensors
     page = k_pages.shape[2]
     ids = table[b, :-(-n // page)].long().cpu().numpy()
@@ -175,21 +183,26 @@ def sequence(cache_tensors, table, b, n):
         x = values_of(pages[torch.as_tensor(ids, device=pages.device)]
                       if pages.dtype == torch.uint8 else
                       pages.view(torch.uint8)[torch.as_tensor(ids, device=pages.device)])
-        x = x * scale.double().cpu().numpy()[ids][:, :, None, None]
-        out.append(x.transpose(1, 0, 2, 3).reshape(x.shape[1], -1, D)[:, :n])
-    return out
+        s = scale.double().cpu().numpy()[ids]                       # [pages, Hkv]
+        per = 128 // page
+        tops = np.maximum.reduceat(np.abs(s), np.arange(0, len(ids), per), axis=0)
+        u = np.repeat(tops, per, axis=0)[:len(ids)]
+        for y in (x * s[:, :, None, None], np.abs(x) * u[:, :, None, None]):
+            out.append(y.transpose(1, 0, 2, 3).reshape(x.shape[1], -1, D)[:, :n])
+    return out[0], out[2], out[3]
 
 
-def decode_bound(q, K, V, ref, keep_keys):
-    """|o - ref| bound of one query head: q [128], K, V [n, 128], keep_keys [n] bool."""
+def decode_bound(q, K, V, ref, keep_keys, coarse=None):
+    """|o - ref| bound of one query head: q [128], K, V [n, 128], keep_keys [n] bool,
+    coarse: u |v8| [n, 128] (|V| when None)."""
     k = K[keep_keys]
     A = (np.abs(k) @ np.abs(q)).max() / math.sqrt(D)
     B = 2.0 ** -29 * np.abs(q).max() * np.abs(k).sum(-1).max() / math.sqrt(D)
-    s = np.where(keep_keys, (K @ q) / math.sqrt(D), -np.inf)
+    s = (k @ q) / math.sqrt(D)
     p = np.exp(s - s.max())
     p /= p.sum()
-    S = p @ np.abs(V)
-    edges = np.arange(0, len(p), 32)
-    U = np.maximum.reduceat(p, edges) @ np.add.reduceat(np.abs(V), edges, axis=0)
+    v = np.abs(V[keep_keys])
+    S = p @ v
+    U = p.max() * (v if coarse is None else coarse[keep_keys]).sum(0)
     return 2.0 ** -8 * np.abs(ref) + S * (2.0 ** -11 + 4 * (129 * 2.0 ** -23 * A + B) + 2.0 ** -20) \
-        + 2.0 ** -26 * U
+        + 2.0 ** -30 * U

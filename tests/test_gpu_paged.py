@@ -97,7 +97,7 @@ def check_decode(tensors, lens, q, o, tau, per_head, kept=None, bits=None, skip=
             assert (on[b] == 0).all() and (kept is None or int(kept[b].abs().sum()) == 0)
             assert bits is None or int(bits[b].abs().sum()) == 0
             continue
-        K, V = R.sequence((k, v, ks, vs), t, b, n)
+        K, V, coarse = R._sequence((k, v, ks, vs), t, b, n)
         ref = oracle.decode(qn[b], K, V, tau=tau, per_head=per_head, want_margin=True)
         nt = oracle.n_blocks(n, 128)
         for h in range(q.shape[1]):
@@ -109,7 +109,7 @@ def check_decode(tensors, lens, q, o, tau, per_head, kept=None, bits=None, skip=
                     continue
                 assert int(kept[b, unit]) == int(ref["keep"][unit].sum())
             keys = np.repeat(ref["keep"][unit].astype(bool), 128)[:n]
-            tol = R.decode_bound(qn[b, h], K[h // G], V[h // G], ref["o"][h], keys)
+            tol = R.decode_bound(qn[b, h], K[h // G], V[h // G], ref["o"][h], keys, coarse[h // G])
             assert (np.abs(on[b, h] - ref["o"][h]) <= tol).all(), (b, h, n)
             compared += 1
     return compared
@@ -294,6 +294,126 @@ def test_decode_pages_beyond_32_bit_offsets():
         tol = R.decode_bound(as_f64(q)[0, h], kv[0][h // 2], kv[1][h // 2], r["o"][h],
                              np.ones(n, bool))
         assert (np.abs(as_f64(o)[0, h] - r["o"][h]) <= tol).all()
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+def test_decode_statistics_in_several_stretches(per_head):
+    """A cache long enough that the rule is replayed in stretches (eight heads: 1280 tiles at a
+    time), with keys of the sequence's queries here and there."""
+    n, page, G = 200_003, 128, 8
+    tensors = filled([n], 1, page, "plain", 71, peak=False)
+    k, _, _, _, t = tensors
+    g = gen(72)
+    q = (torch.randn((1, G, 128), device="cuda", generator=g) * 0.4).to(bf16)
+    for i, pos in enumerate(torch.randint(0, n, (24,), generator=g, device="cuda").tolist()):
+        x = q[0, i % G].float()
+        k.view(torch.uint8)[int(t[0, pos // page]), 0, pos % page] = \
+            (x * 400).clamp(-448, 448).to(f8).view(torch.uint8)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor([n], dtype=i32, device="cuda")
+    o, kept, bits = mala.mala_decode_paged(q, cache, sl, tau=0.5, per_head=per_head, trace=True)
+    mala.mala_check()
+    assert int(kept.min()) > 1
+    assert check_decode(tensors, [n], q, o, 0.5, per_head, kept, bits) >= 0.7 * G
+
+
+def test_decode_a_length_above_the_bound_within_its_tile():
+    lens = [300, 299, 300]
+    tensors = filled(lens, 1, 32, "plain", 73)
+    q = torch.randn((3, 2, 128), device="cuda", generator=gen(74)).to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    for tau in (1.0, 0.0):
+        o = mala.mala_decode_paged(q, cache, sl, tau=tau, max_seqlen=299)
+        with pytest.raises(mala.MalaError, match="MALA_ERR_BAD_PAGE"):
+            mala.mala_check()
+        assert torch.isnan(o[0]).all() and torch.isnan(o[2]).all() and not torch.isnan(o[1]).any()
+
+
+def test_decode_a_nan_value_shows_only_in_heads_that_keep_its_tile():
+    """per_head: a value that is NaN in a tile that one head keeps and the others skip."""
+    n, page = 1000, 64
+    tensors = list(filled([n], 1, page, "plain", 75, peak=False))
+    k, v, ks, vs, t = tensors
+    q = (torch.randn((1, 4, 128), device="cuda", generator=gen(76)) * 0.3).to(bf16)
+    ks[:] = 2.0 ** -6
+    u8 = k.view(torch.uint8)
+    pid = int(t[0, 1])
+    u8[pid, 0, 5] = (q[0, 2].float() * 1500).clamp(-448, 448).to(f8).view(torch.uint8)  # tile 0, head 2
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor([n], dtype=i32, device="cuda")
+    clean, kept, bits = mala.mala_decode_paged(q, cache, sl, tau=900.0, per_head=True, trace=True)
+    keeps = [bool(int(bits[0, h, 0]) & 1) for h in range(4)]
+    assert keeps[2] and not all(keeps)
+    v.view(torch.uint8)[pid, 0, 9, 17] = 0x7f
+    o = mala.mala_decode_paged(q, cache, sl, tau=900.0, per_head=True)
+    mala.mala_check()
+    for h in range(4):
+        assert bool(torch.isnan(o[0, h, 17])) == keeps[h]
+        rest = [i for i in range(128) if i != 17]
+        assert torch.equal(o[0, h, rest], clean[0, h, rest])
+
+
+def test_decode_queries_that_are_not_finite_and_of_all_sizes():
+    lens = [500]
+    tensors = filled(lens, 1, 16, "plain", 77, peak=False)
+    q = torch.randn((1, 8, 128), device="cuda", generator=gen(78))
+    q[0, 1, 3] = float("inf")
+    q[0, 3, 100] = float("nan")
+    q[0, 4] = q[0, 4] * 2.0 ** -120
+    q[0, 5, 1:] *= 2.0 ** -18  # one value far above the rest
+    q[0, 6] = 0
+    q = q.to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    o = mala.mala_decode_paged(q, cache, sl, tau=0.0)
+    mala.mala_check()
+    assert torch.isnan(o[0, [1, 3]]).all()
+    K, V, coarse = R._sequence(tensors[:4], tensors[4], 0, 500)
+    qn, on = as_f64(q), as_f64(o)
+    for h in (0, 2, 4, 5, 6, 7):
+        ref = oracle.decode(qn[0, h:h + 1], K, V, tau=0.0)["o"][0]
+        tol = R.decode_bound(qn[0, h], K[0], V[0], ref, np.ones(500, bool), coarse[0])
+        assert (np.abs(on[0, h] - ref) <= tol).all(), h
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode_pages_of_very_different_scales(page):
+    lens = [700, 130]
+    tensors = filled(lens, 2, page, "plain", 79, peak=False)
+    vs = tensors[3]
+    vs *= torch.exp2(torch.randint(-12, 13, vs.shape, device="cuda", generator=gen(80)).float())
+    vs[int(tensors[4][0, 1])] = 0.0
+    q = torch.randn((2, 6, 128), device="cuda", generator=gen(81)).to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    for tau in (1.0, 0.0):
+        o, kept, bits = mala.mala_decode_paged(q, cache, sl, tau=tau, trace=True)
+        mala.mala_check()
+        assert check_decode(tensors, lens, q, o, tau, False, kept, bits) >= 0.9 * 12
+
+
+def test_decode_beside_a_prefill_on_another_stream():
+    """Both kernels want tensor memory; whichever an SM runs first, both end."""
+    g = gen(82)
+    lens = [2000] * 8
+    tensors = filled(lens, 4, 64, "plain", 83)
+    q = torch.randn((8, 16, 128), device="cuda", generator=g).to(bf16)
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    Q, K, V = (torch.randn((1, 8, 4096, 128), device="cuda", generator=g).to(bf16) for _ in range(3))
+    want = mala.mala_decode_paged(q, cache, sl, tau=1.0)
+    O, _ = mala.mala_fwd(Q, K, V, tau=1.0)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    outs, fwd = [], []
+    for _ in range(5):
+        with torch.cuda.stream(other):
+            fwd.append(mala.mala_fwd(Q, K, V, tau=1.0)[0])
+        outs.append(mala.mala_decode_paged(q, cache, sl, tau=1.0))
+    torch.cuda.synchronize()
+    mala.mala_check()
+    assert all(torch.equal(x, want) for x in outs) and all(torch.equal(x, O) for x in fwd)
 
 
 # ---------------------------------------------------------------------------- append
