@@ -61,6 +61,8 @@ constexpr int MAXC = 16;              // blocks of a cluster
 constexpr int NMETA = 16;             // tiles whose scales are held
 constexpr int TERMS = 4;
 constexpr int SBUF = 4;                // buffers of scores in tensor memory
+// SBUF buffers of S and two of O; a power of two
+__host__ __device__ constexpr uint32_t tmem_columns(int GH) { return 8 * TERMS * GH; }
 
 struct Params {
   Pool pool;
@@ -304,12 +306,12 @@ __device__ __forceinline__ void store_p(unsigned char* buf, int key, const float
 }
 
 // The load warp: tiles one after the other into the ring. `place(i)`: the i-th tile's first
-// position and heads. With values, a tile's V follows its K. `seq`: stages used so far.
-template <typename Sh, typename Place>
+// position and heads. VALUES: a tile's V follows its K. `seq`: stages used so far.
+template <bool VALUES, typename Sh, typename Place>
 __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* tmK,
                                            const CUtensorMap* tmV, unsigned char* ring, Sh& sh,
-                                           int b, int h, int len, int tiles, bool values,
-                                           uint32_t seq, uint32_t meta0, Place place) {
+                                           int b, int h, int len, int tiles, uint32_t seq,
+                                           uint32_t meta0, Place place) {
   const int lane = threadIdx.x & 31;
   const int per_log2 = 7 - pool.page_log2, per = 1 << per_log2;  // pages of a tile
   const int batch = 32 >> per_log2, sub = lane & (per - 1);
@@ -336,7 +338,7 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
       }
       if (id >= 0) {
         ks = pool.k_scale[(long long)id * pool.Hkv + h];
-        if (values) vs = pool.v_scale[(long long)id * pool.Hkv + h];
+        if (VALUES) vs = pool.v_scale[(long long)id * pool.Hkv + h];
       }
     }
     const int n = min(batch, tiles - i0);
@@ -344,12 +346,17 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
       const bool mine = (lane >> per_log2) == j;
       const uint32_t bytes =
           (uint32_t)__popc(__ballot_sync(0xffffffffu, mine && id >= 0)) * (uint32_t)pool.page * D;
-      for (int w = 0; w < (values ? 2 : 1); ++w, ++seq) {
+      for (int w = 0; w < (VALUES ? 2 : 1); ++w, ++seq) {
         const uint32_t st = seq % NST, turn = seq / NST;
         bool ok = true;
         if (lane == 0 && turn > 0)
           ok = mbar_wait(smem_u32(&sh.empty[st]), (turn - 1) & 1, abort, 0x511);
         if (!__shfl_sync(0xffffffffu, (int)ok, 0)) return false;
+        if (mine && id >= 0)
+          sm100::tma_load_4d(smem_u32(ring) + st * TILE_BYTES + (uint32_t)(sub * pool.page) * D,
+                             w ? tmV : tmK, 0, 0, h, id, smem_u32(&sh.full[st]));
+        // the scales may still be on their way; the tile counts as there behind them (the bytes may
+        // come before they are expected: the phase waits for the arrival)
         if (mine && w == 0) {  // sixteen tiles are held, the softmax is ten behind at most
           Meta& m = sh.meta[(meta0 + (uint32_t)(i0 + j)) % NMETA];
           if (sub == 0) {
@@ -363,10 +370,6 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
         }
         __syncwarp();
         if (lane == 0) mbar_expect_tx(smem_u32(&sh.full[st]), bytes);
-        __syncwarp();
-        if (mine && id >= 0)
-          sm100::tma_load_4d(smem_u32(ring) + st * TILE_BYTES + (uint32_t)(sub * pool.page) * D,
-                             w ? tmV : tmK, 0, 0, h, id, smem_u32(&sh.full[st]));
       }
     }
   }
@@ -437,11 +440,17 @@ __device__ __forceinline__ bool issue_o(Shared<GH>& sh, const Issuer& is, uint32
   __syncwarp();
   return true;
 }
-// Scores two tiles ahead of the values.
+// Scores two tiles ahead of the values. `held`: the scores are there from before, and the i-th
+// tile is the block's held[i].
 template <int GH>
 __device__ __forceinline__ bool issue_pairs(Shared<GH>& sh, const Issuer& is, int tiles, uint32_t seq0,
-                                            uint32_t s0) {
+                                            uint32_t s0, const uint32_t* held) {
   bool ok = true;
+  if (held) {
+    for (int i = 0; i < tiles && ok; ++i)
+      ok = issue_o<GH>(sh, is, seq0 + 2 * (held[i] & 0xffffffu) + 1, i);
+    return ok;
+  }
   for (int i = 0; i < 2 && i < tiles && ok; ++i) ok = issue_s<GH>(sh, is, seq0 + 2 * i, s0 + i);
   for (int i = 0; i < tiles && ok; ++i) {
     ok = issue_o<GH>(sh, is, seq0 + 2 * i + 1, i);
@@ -506,23 +515,25 @@ __device__ __forceinline__ void add_o(Shared<GH>& sh, uint32_t i, const float (&
 // max; else it runs along, and l is the mass of this thread's keys.
 template <int GH, bool FIXED>
 __device__ __forceinline__ void softmax_pv(Shared<GH>& sh, unsigned char* ring, int len, int tiles,
-                                           uint32_t s0, uint32_t seq0, const float (&undo)[GH],
-                                           float (&mref)[GH], float (&l)[GH], float (&out)[GH]) {
+                                           uint32_t s0, uint32_t seq0, const uint32_t* held,
+                                           const float (&undo)[GH], float (&mref)[GH],
+                                           float (&l)[GH], float (&out)[GH]) {
   const int key = threadIdx.x, warp = key >> 5;
   float f[GH];  // the tile before: what its O counts
 #pragma unroll
   for (int g = 0; g < GH; ++g) f[g] = 0.f;
   uint32_t heads_before = 0;
   for (int i = 0; i < tiles; ++i) {
-    const Meta& m = sh.meta[(s0 + (uint32_t)i) % NMETA];
-    const uint32_t s = s0 + (uint32_t)i;
+    const uint32_t nth = FIXED && held ? held[i] & 0xffffffu : (uint32_t)i;
+    const uint32_t s = s0 + nth;
+    const Meta& m = sh.meta[s % NMETA];
     uint32_t raw[TERMS * GH];
     start_scores<GH>(sh, s, raw);
     // what is wanted of m is read before the products' buffer is given back: the load warp may
     // overwrite it later
     const float ks = m.k[key >> 4];
     const int left = len - m.pos;
-    const uint32_t heads = FIXED ? m.heads : 0xffu;
+    const uint32_t heads = FIXED ? (held ? held[i] >> 24 : m.heads) : 0xffu;
     // pages of different scales: V's bytes count u, the largest, and P takes the rest
     const float4 v0 = *reinterpret_cast<const float4*>(m.v);
     const float4 v1 = *reinterpret_cast<const float4*>(m.v + 4);
@@ -571,7 +582,7 @@ __device__ __forceinline__ void softmax_pv(Shared<GH>& sh, unsigned char* ring, 
     if (left < T) {
       // rows behind the sequence hold anything, and a product with a NaN is NaN even where P
       // is zero
-      const uint32_t seq = seq0 + 2u * (uint32_t)i + 1u, st = seq % NST;
+      const uint32_t seq = seq0 + 2u * nth + 1u, st = seq % NST;
       warp_wait(&sh.full[st], (seq / NST) & 1, &sh.abort, 0x519);
       if (key >= left)
 #pragma unroll
@@ -589,6 +600,13 @@ __device__ __forceinline__ void softmax_pv(Shared<GH>& sh, unsigned char* ring, 
   if (tiles > 0) add_o<GH>(sh, tiles - 1, f, heads_before, out);
 }
 
+template <int GH>
+__device__ __forceinline__ void free_tmem(const Shared<GH>& sh) {
+  __syncwarp();
+  sm100::tc_fence_after();
+  sm100::tmem_dealloc(sh.tmem, tmem_columns(GH));
+}
+
 // Joins the blocks' outputs and writes o = sum / l: thread tid of the softmax warps has
 // dimension tid of every head. dense: the blocks' references differ (sh.mfin), else
 // sh.lfin is the whole cluster's mass. Each block owns some of the dimensions, and the others
@@ -601,6 +619,7 @@ __device__ __forceinline__ void join_and_store(const Params& p, Shared<GH>& sh,
   Join& jn = sh.join;
   const float nan = __int_as_float(0x7fc00000);
   if (C == 1) {
+    if ((tid >> 5) == W_TMEM) free_tmem(sh);
     if (tid < NC)
 #pragma unroll
       for (int g = 0; g < GH; ++g)
@@ -623,6 +642,9 @@ __device__ __forceinline__ void join_and_store(const Params& p, Shared<GH>& sh,
                             make_float2(sh.mfin[g], sh.lfin[g]));
   }
   cluster_arrive();
+  // given back here, by a warp whose lanes are together (behind the loop below they need not be,
+  // and a deallocation by part of a warp never ends)
+  if ((tid >> 5) == W_TMEM) free_tmem(sh);
   cluster_wait();
   for (int e = tid; e < G * each; e += NT) {
     const int g = e / each, i = e - g * each, dim = (int)rank * each + i;
@@ -687,7 +709,7 @@ struct Walk {
 // per head.
 template <int GH>
 __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, unsigned char* smem,
-                                            float2* stats, uint32_t* keep, uint32_t* list,
+                                            bool resident, float2* stats, uint32_t* keep, uint32_t* list,
                                             long long grp, int len, int nt, uint32_t rank) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.G, GP = p.GP, C = p.C;
@@ -812,7 +834,16 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
   __syncwarp();
   __syncthreads();
   const int live = (nt + 31) / 32;
-  if (warp == 0) {  // the n-th kept tile (in the order of positions) is block n mod C's
+  if (warp == 0 && resident) {  // its own tiles, as many as are kept
+    const int t = lane * C + (int)rank;
+    uint32_t heads = 0;
+    if (lane < 2 && t < nt)
+      for (int u = 0; u < units; ++u)
+        if ((keep[u * words + (t >> 5)] >> (t & 31)) & 1u) heads |= p.per_head ? 1u << u : 0xffu;
+    const uint32_t kept = __ballot_sync(0xffffffffu, heads != 0u);
+    if (heads) list[__popc(kept & ((1u << lane) - 1u))] = (uint32_t)lane | heads << 24;
+    if (lane == 0) sh.items = __popc(kept);
+  } else if (warp == 0) {  // the n-th kept tile (in the order of positions) is block n mod C's
     int count = 0;
     for (int w0 = 0; w0 < live; w0 += 32) {
       uint32_t any = 0;
@@ -860,7 +891,7 @@ template <int GH, bool RULE>
 __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ CUtensorMap tmK,
                                                        const __grid_constant__ CUtensorMap tmV,
                                                        const Params p) {
-  constexpr uint32_t TCOLS = 8 * TERMS * GH;  // SBUF buffers of S and two of O; a power of two
+  constexpr uint32_t TCOLS = tmem_columns(GH);
   static_assert(SBUF + 2 <= 8 && 2 * TCOLS <= 512, "two blocks share an SM's tensor memory");
   extern __shared__ unsigned char smem[];
   Shared<GH>& sh = *reinterpret_cast<Shared<GH>*>(smem + RING);
@@ -946,11 +977,17 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
   issuer.tmem = warp == W_MMA ? __shfl_sync(0xffffffffu, sh.tmem, 0) : 0u;
 
   if constexpr (RULE) {
-    // ---- A: statistics
+    // ---- A: statistics. A block with at most two tiles loads their values as well and keeps
+    // all of it, scores in tensor memory included: C then has nothing to wait for (some values
+    // that nobody wants are read, while a block waits for little else than latency).
+    const bool resident = nt <= 2 * C;
     if (warp == W_LOAD) {
-      ok = load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, false, 0u, 0u, own_tile);
+      if (resident)
+        ok = load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, own_tile);
+      else
+        ok = load_tiles<false>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, own_tile);
     } else if (warp == W_MMA) {
-      for (int i = 0; i < tiles && ok; ++i) ok = issue_s<GH>(sh, issuer, i, i);
+      for (int i = 0; i < tiles && ok; ++i) ok = issue_s<GH>(sh, issuer, resident ? 2 * i : i, i);
     } else if (warp < 4) {
       // NB tiles at a time: their loads and reductions overlap
       constexpr int NB = GH == 4 ? 4 : 2;
@@ -1031,32 +1068,35 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     }
 
     // ---- B
-    replay_rule<GH>(p, sh, smem, stats, keep, list, grp, len, nt, rank);
+    replay_rule<GH>(p, sh, smem + (resident ? 4 * TILE_BYTES : 0), resident, stats, keep, list, grp, len,
+                    nt, rank);
 
     // ---- C: values of this block's kept tiles
     const int items = sh.items;
-    const uint32_t done = (uint32_t)tiles;
+    const uint32_t done = resident ? 0u : (uint32_t)tiles;
+    const uint32_t* held = resident ? list : nullptr;
     if (warp == W_LOAD) {
       auto kept_tile = [&](int i, int& pos, uint32_t& heads) {
         const uint32_t x = list[i];
         pos = (int)(x & 0xffffffu) * T;
         heads = x >> 24;
       };
-      if (ok) load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, items, true, done, done, kept_tile);
+      if (ok && !resident)
+        load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, items, done, done, kept_tile);
     } else if (warp == W_MMA) {
-      if (ok) issue_pairs<GH>(sh, issuer, items, done, done);
+      if (ok) issue_pairs<GH>(sh, issuer, items, done, done, held);
     } else if (warp < 4) {
 #pragma unroll
       for (int g = 0; g < GH; ++g) mref[g] = g < G ? sh.mfin[g] : 0.f;
-      softmax_pv<GH, true>(sh, smem, len, items, done, done, undo, mref, l, out);
+      softmax_pv<GH, true>(sh, smem, len, items, done, done, held, undo, mref, l, out);
     }
   } else {
     if (warp == W_LOAD) {
-      ok = load_tiles(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, true, 0u, 0u, own_tile);
+      ok = load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, own_tile);
     } else if (warp == W_MMA) {
-      issue_pairs<GH>(sh, issuer, tiles, 0u, 0u);
+      issue_pairs<GH>(sh, issuer, tiles, 0u, 0u, nullptr);
     } else if (warp < 4) {
-      softmax_pv<GH, false>(sh, smem, len, tiles, 0u, 0u, undo, mref, l, out);
+      softmax_pv<GH, false>(sh, smem, len, tiles, 0u, 0u, nullptr, undo, mref, l, out);
       // the block's mass per head: every thread has its own keys'
 #pragma unroll
       for (int g = 0; g < GH; ++g) {
@@ -1077,12 +1117,6 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
   sm100::tc_fence_before();
   __syncwarp();
   __syncthreads();
-  // given back here, by a warp whose lanes are together (behind the join's loops they need not
-  // be, and a deallocation by part of a warp never ends)
-  if (warp == W_TMEM) {
-    sm100::tc_fence_after();
-    sm100::tmem_dealloc(sh.tmem, TCOLS);
-  }
   if (!RULE && C > 1) cluster_wait();  // the other blocks run
   join_and_store<GH>(p, sh, out, rank, o, !RULE);
   if (!RULE && rank == 0) {  // every tile is kept
