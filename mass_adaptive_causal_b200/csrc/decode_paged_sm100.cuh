@@ -49,11 +49,12 @@ using sm100::smem_u32;
 
 constexpr int T = 128;
 constexpr int GMAX = 8;
-constexpr int NT = 256;               // warps 0 - 3 softmax, 4 loads, 5 products, 6 holds the tensor
-                                      // memory, 6 and 7 help in B
+constexpr int NT = 256;               // warps 0 - 3 softmax, 4 and 7 load, 5 products, 6 holds the
+                                      // tensor memory
 constexpr int NC = 128;               // softmax threads
-static_assert(NT - 32 == 224, "the number in the second named barrier");
-constexpr int W_LOAD = 4, W_MMA = 5, W_TMEM = 6;
+static_assert(NT - 64 == 192, "the number in the second named barrier");
+constexpr int W_MMA = 5, W_TMEM = 6;
+constexpr int W_LOAD = 4, W_LOAD2 = 7;  // even and odd tiles: one warp's loop bounded a block's rate
 constexpr uint32_t TILE_BYTES = T * D;
 constexpr int NST = 5;                // ring stages (tiles)
 constexpr uint32_t RING = NST * TILE_BYTES;
@@ -305,21 +306,23 @@ __device__ __forceinline__ void store_p(unsigned char* buf, int key, const float
         make_uint4(x[4 * n], x[4 * n + 1], x[4 * n + 2], x[4 * n + 3]);
 }
 
-// The load warp: tiles one after the other into the ring. `place(i)`: the i-th tile's first
-// position and heads. VALUES: a tile's V follows its K. `seq`: stages used so far.
+// A load warp: every second tile (`who`: the even or the odd ones) into the ring, one after
+// the other. `place(i)`: the i-th tile's first position and heads. VALUES: a tile's V follows
+// its K. `seq0`: stages used before.
 template <bool VALUES, typename Sh, typename Place>
 __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* tmK,
                                            const CUtensorMap* tmV, unsigned char* ring, Sh& sh,
-                                           int b, int h, int len, int tiles, uint32_t seq,
+                                           int b, int h, int len, int tiles, uint32_t seq0,
                                            uint32_t meta0, Place place) {
+  const int who = (threadIdx.x >> 5) == W_LOAD ? 0 : 1;
   const int lane = threadIdx.x & 31;
   const int per_log2 = 7 - pool.page_log2, per = 1 << per_log2;  // pages of a tile
   const int batch = 32 >> per_log2, sub = lane & (per - 1);
   const int32_t* row = pool.table + (long long)b * pool.table_stride;
   volatile int* abort = &sh.abort;
-  for (int i0 = 0; i0 < tiles; i0 += batch) {
+  for (int i0 = who; i0 < tiles; i0 += 2 * batch) {
     // 32 pages at a time, a lane each
-    const int i = i0 + (lane >> per_log2);
+    const int i = i0 + 2 * (lane >> per_log2);
     int pos = 0, id = -1;
     uint32_t heads = 0;
     float ks = 0.f, vs = 0.f;
@@ -341,8 +344,9 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
         if (VALUES) vs = pool.v_scale[(long long)id * pool.Hkv + h];
       }
     }
-    const int n = min(batch, tiles - i0);
+    const int n = min(batch, (tiles - i0 + 1) >> 1);
     for (int j = 0; j < n; ++j) {
+      uint32_t seq = seq0 + (uint32_t)((VALUES ? 2 : 1) * (i0 + 2 * j));
       const bool mine = (lane >> per_log2) == j;
       const uint32_t bytes =
           (uint32_t)__popc(__ballot_sync(0xffffffffu, mine && id >= 0)) * (uint32_t)pool.page * D;
@@ -358,7 +362,7 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
         // the scales may still be on their way; the tile counts as there behind them (the bytes may
         // come before they are expected: the phase waits for the arrival)
         if (mine && w == 0) {  // sixteen tiles are held, the softmax is ten behind at most
-          Meta& m = sh.meta[(meta0 + (uint32_t)(i0 + j)) % NMETA];
+          Meta& m = sh.meta[(meta0 + (uint32_t)(i0 + 2 * j)) % NMETA];
           if (sub == 0) {
             m.pos = pos;
             m.heads = heads;
@@ -954,7 +958,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     mref[g] = kNegInf;
     l[g] = out[g] = 0.f;
   }
-  if (warp != W_LOAD) {  // the load warp needs none of this
+  if (warp != W_LOAD && warp != W_LOAD2) {  // the load warps need none of this
     if (warp == W_TMEM) {
       sm100::tmem_alloc(smem_u32(&sh.tmem), TCOLS);
       sm100::tmem_relinquish();
@@ -964,7 +968,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     }
     sm100::tc_fence_before();
     __syncwarp();
-    asm volatile("barrier.cta.sync 2, 224;" ::: "memory");
+    asm volatile("barrier.cta.sync 2, 192;" ::: "memory");
     sm100::tc_fence_after();
 #pragma unroll
     for (int g = 0; g < GH; ++g) undo[g] = sh.undo[g];
@@ -981,7 +985,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     // all of it, scores in tensor memory included: C then has nothing to wait for (some values
     // that nobody wants are read, while a block waits for little else than latency).
     const bool resident = nt <= 2 * C;
-    if (warp == W_LOAD) {
+    if (warp == W_LOAD || warp == W_LOAD2) {
       if (resident)
         ok = load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, own_tile);
       else
@@ -1075,7 +1079,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     const int items = sh.items;
     const uint32_t done = resident ? 0u : (uint32_t)tiles;
     const uint32_t* held = resident ? list : nullptr;
-    if (warp == W_LOAD) {
+    if (warp == W_LOAD || warp == W_LOAD2) {
       auto kept_tile = [&](int i, int& pos, uint32_t& heads) {
         const uint32_t x = list[i];
         pos = (int)(x & 0xffffffu) * T;
@@ -1091,7 +1095,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
       softmax_pv<GH, true>(sh, smem, len, items, done, done, held, undo, mref, l, out);
     }
   } else {
-    if (warp == W_LOAD) {
+    if (warp == W_LOAD || warp == W_LOAD2) {
       ok = load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, own_tile);
     } else if (warp == W_MMA) {
       issue_pairs<GH>(sh, issuer, tiles, 0u, 0u, nullptr);
