@@ -75,14 +75,20 @@ inline bool make_page_map(CUtensorMap* m, const void* base, const paged::Pool& p
   return r == CUDA_SUCCESS;
 }
 
-// Blocks of a decode cluster, 0 when the statistics of the longest sequence do not fit.
+// Blocks of a decode cluster: the largest power of two that leaves no more than 1.3 waves of
+// blocks (two to an SM), 0 when the statistics of the longest sequence do not fit. More splits a
+// long sequence finer but adds blocks that cost 8 us each and run in a second wave: 16 x 8 heads
+// x 8192 keys, exact: 2 blocks 48 us, 4: 57 us; 24 x 8 heads ragged to 16384: 1 block 83 us, 2: 39 us,
+// 4: 51 us. Clusters of 16 blocks do not pack: the chip holds 14, not 18, so they are for
+// fewer groups than that (16 groups of 16384 keys: 8 blocks 41 us, 16: 59 us).
 inline int decode_cluster(const pdec::Params& p, long long groups, bool rule, size_t* smem) {
   int best = 0;
   for (int C = 1; C <= pdec::MAXC; C *= 2) {
     const size_t need = pdec::smem_bytes(p.G, p.max_tiles, C, p.per_head, rule);
     if (need > pdec::MAX_SMEM) continue;
     const long long slots = (long long)sm_count() * (need <= 113 * 1024 ? 2 : 1);
-    if (best > 0 && (10 * groups * C > 13 * slots || C / 2 >= p.max_tiles)) break;
+    const long long room = C == 16 ? 10 * slots / 13 : 13 * slots / 10;
+    if (best > 0 && (groups * C > room || C / 2 >= p.max_tiles)) break;
     best = C;
     *smem = need;
   }
