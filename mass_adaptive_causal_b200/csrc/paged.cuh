@@ -124,24 +124,35 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* x) {
 }
 
 // A thread holds sixteen of a row's 128 values: two chunks of eight, c0 and
-// c1, chosen so that every rotated pair lies within the thread.
+// c1, chosen so that every rotated pair lies within the thread and that neighbours' chunks lie
+// side by side (a store then fills whole sectors): of the rotated part the t-th chunk of
+// each half, of the rest likewise. Pairs (x_i, x_{i + rot/2}) have their elements in c0 and
+// c1, pairs (x_2i, x_2i+1) both in one.
 struct Chunks {
   int c0, c1;   // first dimension of each chunk
-  int freq;     // index of the first of its eight frequencies, -1: not rotated
+  bool rotated;
 };
-__device__ __forceinline__ Chunks chunks_of(int t, int rot, int interleaved) {
+__device__ __forceinline__ Chunks chunks_of(int t, int rot) {
   Chunks c;
   const int pairs = rot >> 4;  // threads that rotate
-  c.freq = t < pairs ? 8 * t : -1;
-  if (interleaved || t >= pairs) {  // (x_2i, x_2i+1), or the part that is not rotated
-    c.c0 = 16 * t;
-    c.c1 = 16 * t + 8;
-  } else {  // (x_i, x_{i + rot/2})
-    c.c0 = 8 * t;
-    c.c1 = 8 * t + (rot >> 1);
-  }
+  c.rotated = t < pairs;
+  c.c0 = c.rotated ? 8 * t : rot + 8 * (t - pairs);
+  c.c1 = c.c0 + ((c.rotated ? rot : 128 - rot) >> 1);
   return c;
 }
+// The thread's k-th frequency (of eight), and whose f is and which.
+template <bool INTERLEAVED>
+__device__ __forceinline__ int freq_of(int t, int k, int rot) {
+  if (!INTERLEAVED) return 8 * t + k;
+  return 4 * t + (k < 4 ? k : (rot >> 2) + k - 4);
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ int freq_slot(int f, int rot) {  // 8 t + k
+  if (!INTERLEAVED) return f;
+  const int half = f >= rot >> 2 ? 1 : 0, g = f - half * (rot >> 2);
+  return 8 * (g >> 2) + 4 * half + (g & 3);
+}
+
 // Two floats side by side, and the two-at-a-time instructions on them.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float a, float b) {
@@ -237,7 +248,7 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
   const int row0 = begin - (slot << p.pool.page_log2), n = end - begin;
   const long long tok0 = (long long)first + (begin - start);
   const int tid = threadIdx.x, t = tid & 7, r0 = (tid % LPU) >> 3;
-  const Chunks ch = chunks_of(t, p.rot, INTERLEAVED);
+  const Chunks ch = chunks_of(t, p.rot);
   const int h0 = blockIdx.z * p.heads, nh = min(p.heads, p.pool.Hkv - h0);
   const int id = page_of(p.pool, b, slot);  // no page: its rows are left out, q is rotated all the same
 
@@ -311,15 +322,17 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
       float4 cs;
       turn(begin + r, p.inv_freq[f], cs.x, cs.z);
       turn(begin + r, p.inv_freq[f + 1], cs.y, cs.w);
-      table[r * 32 + ((f >> 1) & 3) * 8 + (f >> 3)] = cs;
+      const int k = freq_slot<INTERLEAVED>(f, p.rot);
+      table[r * 32 + ((k >> 1) & 3) * 8 + (k >> 3)] = cs;
     }
     __syncthreads();
   }
   float4 own[TABLE ? 1 : PASSES][4];
-  if (!TABLE && ch.freq >= 0) {
+  if (!TABLE && ch.rotated) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = make_float2(p.inv_freq[ch.freq + 2 * j], p.inv_freq[ch.freq + 2 * j + 1]);
+      const float2 f = make_float2(p.inv_freq[freq_of<INTERLEAVED>(t, 2 * j, p.rot)],
+                                   p.inv_freq[freq_of<INTERLEAVED>(t, 2 * j + 1, p.rot)]);
 #pragma unroll
       for (int ps = 0; ps < (TABLE ? 1 : PASSES); ++ps)
         if (ps < n) {
@@ -341,7 +354,7 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
   };
   auto store_q = [&](int ps, int r, __nv_bfloat16* dst) {
     uint4 w[2] = {raw[ps][0], raw[ps][1]};  // not rotated: bit for bit
-    if (ch.freq >= 0) {
+    if (ch.rotated) {
       float x[16];
       values(ps, r, true, x);
       uint32_t* z = reinterpret_cast<uint32_t*>(w);
@@ -360,7 +373,7 @@ __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams
     const bool more = u + UNITS < total;
     aim(u + UNITS);
     const bool kv = u < 2 * nh, keys = u < nh;
-    const bool rotates = (keys || !kv) && ch.freq >= 0;
+    const bool rotates = (keys || !kv) && ch.rotated;
     if (u0 < 2 * nh) {  // some of the block's units are K or V
       const bool store = kv && id >= 0;
       const int h = h0 + (keys ? u : u - nh);
