@@ -365,7 +365,8 @@ mala_status mala_cache_append(const mala_paged_cache* cache, const void* k,
  * relative to the largest of them. Sums, maxima and masses are float32.
  * No workspace. Supported: 1 <= Hq / Hkv <= 8, batch, Hkv <= 65535;
  * MALA_ERR_TOO_LARGE when the statistics of max_seqlen do not fit in the shared
- * memory of a cluster of 16 blocks (above 2.9 million tokens at Hq / Hkv = 8).
+ * memory of a cluster of 16 blocks (beyond 3 million tokens at Hq / Hkv = 8;
+ * tau = 0 has no such bound).
  */
 mala_status mala_decode_paged(const mala_paged_cache* cache, const void* q,
                               void* o, const int32_t* seq_lens, int batch,

@@ -784,10 +784,15 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
         open &= ~(1u << bit);
         const int next = 31 - __clz(open | 1u);
         const float2 y = at[next * GP + seen];  // on its way while this one is decided
-        if (__any_sync(0xffffffffu, !(x.x < w.bound))) {  // a NaN keeps
-          word |= 1u << bit;
-          w.take(x, thr);
-        }
+        // nearly every tile that is left is kept: what it would make of the state is worked out beside
+        // the vote, and taken over without a branch
+        Walk kept = w;
+        kept.take(x, thr);
+        const bool take = __any_sync(0xffffffffu, !(x.x < w.bound));  // a NaN keeps
+        word |= (take ? 1u : 0u) << bit;
+        w.m = take ? kept.m : w.m;
+        w.l = take ? kept.l : w.l;
+        w.bound = take ? kept.bound : w.bound;
         bit = next;
         x = y;
       }

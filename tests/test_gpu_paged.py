@@ -416,6 +416,32 @@ def test_decode_beside_a_prefill_on_another_stream():
     assert all(torch.equal(x, want) for x in outs) and all(torch.equal(x, O) for x in fwd)
 
 
+@pytest.mark.parametrize("per_head", [False, True])
+def test_decode_bounds_of_millions_of_tokens(per_head):
+    """Short sequences under a table that could hold millions of tokens: the statistics' room
+    follows the bound; beyond it the call is refused, but for exact attention."""
+    lens, page = [700, 129], 128
+    k, v, ks, vs, t = filled(lens, 2, page, "plain", 84)
+    wide = torch.full((2, 40000), -1, dtype=i32, device="cuda")
+    wide[:, :t.shape[1]] = t
+    q = torch.randn((2, 16, 128), device="cuda", generator=gen(85)).to(bf16)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    small = mala.PagedCache(k, v, ks, vs, t)
+    large = mala.PagedCache(k, v, ks, vs, wide)
+    want = mala.mala_decode_paged(q, small, sl, tau=1.0, per_head=per_head, max_seqlen=700)
+    for bound in (100_000, 1_000_000, 3_000_000):
+        o, kept, bits = mala.mala_decode_paged(q, large, sl, tau=1.0, per_head=per_head,
+                                               max_seqlen=bound, trace=True)
+        mala.mala_check()
+        assert check_decode((k, v, ks, vs, t), lens, q, o, 1.0, per_head, kept, bits) >= 0.9 * 32
+        assert rel_l2(as_f64(o), as_f64(want)) < 2e-3
+    with pytest.raises(mala.MalaError, match="TOO_LARGE"):
+        mala.mala_decode_paged(q, large, sl, tau=1.0, per_head=per_head)  # 5.1 million tokens
+    o = mala.mala_decode_paged(q, large, sl, tau=0.0, per_head=per_head)
+    mala.mala_check()
+    assert check_decode((k, v, ks, vs, t), lens, q, o, 0.0, per_head) == 32
+
+
 # ---------------------------------------------------------------------------- append
 def projection(T, Hq, Hkv, g, size=1.0):
     x = torch.randn((T, Hq + 2 * Hkv, 128), device="cuda", generator=g) * size
