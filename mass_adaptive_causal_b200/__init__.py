@@ -627,7 +627,7 @@ def mala_decode_paged(q, cache, seq_lens, tau: float = 1.0, scale: float = 0.0,
     """One decode step over a PagedCache, with the rule of mala_decode. q: [batch, Hq,
     128] bf16 (rotated); seq_lens: int32 [batch], the current token included (0: an
     unused slot, its output is zero); max_seqlen: an upper bound of the lengths (default:
-    what the page table can hold). Returns o like q or, with ``trace=True``, (o, kept_tiles
+    what the page table can hold; the work is split by it, so a close one is faster). Returns o like q or, with ``trace=True``, (o, kept_tiles
     [batch, Hkv], keep_bits [batch, Hkv, nw]), per query head with ``per_head=True``;
     nw covers max_seqlen."""
     torch = _paged_ready(cache)

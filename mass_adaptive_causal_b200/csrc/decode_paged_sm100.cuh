@@ -25,7 +25,7 @@
 // is widened to f16, which made a warp's integer work the bound at 45% of the copy
 // bandwidth.) The kernel is bound by HBM: 16 x 131072 tokens of 8 heads, tau = 1: 326 us (2.15 GB
 // of K, the measured copy bandwidth); 16 x 8192, tau = 0: 47 us (5.7 TB/s, 87%); short caches by
-// latency: 1 x 1000: 9 us. Two blocks to an SM: while one waits at its ends, the other streams. The other operand is split into four e4m3 terms, 2^4 apart, in columns of
+// latency: 1 x 1000: 8.7 us. Two blocks to an SM: while one waits at its ends, the other streams. The other operand is split into four e4m3 terms, 2^4 apart, in columns of
 // their own, and the columns' sums are joined in float32:
 //  - q, scaled by a power of two per head to have its largest value in [2^7, 2^8): a bf16
 //    value has eight bits, a term carries four, so values within 2^-21 of the largest are
@@ -308,14 +308,25 @@ __device__ __forceinline__ void store_p(unsigned char* buf, int key, const float
         make_uint4(x[4 * n], x[4 * n + 1], x[4 * n + 2], x[4 * n + 3]);
 }
 
+// The table's entry for the lane's first page, before anything is known of the sequence.
+constexpr int kNone = -2;
+__device__ __forceinline__ int early_page(const Pool& pool, int b, int C, uint32_t rank) {
+  const int who = (threadIdx.x >> 5) == W_LOAD ? 0 : 1, lane = threadIdx.x & 31;
+  const int per_log2 = 7 - pool.page_log2;
+  const long long tile = (long long)(who + 2 * (lane >> per_log2)) * C + rank;
+  const long long slot = (tile << per_log2) + (lane & ((1 << per_log2) - 1));
+  return slot < pool.max_pages ? pool.table[(long long)b * pool.table_stride + slot] : -1;
+}
+
 // A load warp: every second tile (`who`: the even or the odd ones) into the ring, one after
 // the other. `place(i)`: the i-th tile's first position and heads. VALUES: a tile's V follows
-// its K. `seq0`: stages used before.
+// its K. `seq0`: stages used before. `early`: the table's entry for the lane's first page of the
+// block's own tiles, read side by side with the sequence's length (kNone: not read).
 template <bool VALUES, typename Sh, typename Place>
 __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* tmK,
                                            const CUtensorMap* tmV, unsigned char* ring, Sh& sh,
                                            int b, int h, int len, int tiles, uint32_t seq0,
-                                           uint32_t meta0, Place place) {
+                                           uint32_t meta0, int early, Place place) {
   const int who = (threadIdx.x >> 5) == W_LOAD ? 0 : 1;
   const int lane = threadIdx.x & 31;
   const int per_log2 = 7 - pool.page_log2, per = 1 << per_log2;  // pages of a tile
@@ -331,10 +342,11 @@ __device__ __forceinline__ bool load_tiles(const Pool& pool, const CUtensorMap* 
     if (i < tiles) {
       place(i, pos, heads);
       const int at = pos + sub * pool.page, slot = at >> pool.page_log2;
-      if (slot < pool.max_pages) id = row[slot];  // whether it is needed or not: len is on its way
-      if (at >= len) {
-        id = -1;
-      } else {
+      if (at < len) {
+        if (early != kNone && i0 == who)
+          id = early;
+        else if (slot < pool.max_pages)
+          id = row[slot];
         if ((unsigned)id >= (unsigned)pool.num_pages) {
           record_bad_page(0x500);
           sh.bad = 1;
@@ -418,8 +430,8 @@ __device__ __forceinline__ bool issue_s(Shared<GH>& sh, const Issuer& is, uint32
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
       mma_e4m3(is.tmem + buf * (TERMS * GH), a + 2 * kk, is.q + 2 * kk, ID, kk > 0);
+    sm100::mma_commit(smem_u32(&sh.empty[st]));  // first: behind the other the block may end
     sm100::mma_commit(smem_u32(&sh.s_full[buf]));
-    sm100::mma_commit(smem_u32(&sh.empty[st]));
   }
   __syncwarp();
   return true;
@@ -440,8 +452,8 @@ __device__ __forceinline__ bool issue_o(Shared<GH>& sh, const Issuer& is, uint32
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4 KB of V, 512 bytes of P
       mma_e4m3(is.tmem + (SBUF + buf) * (TERMS * GH), a + 256 * kk, b + 32 * kk, ID, kk > 0);
+    sm100::mma_commit(smem_u32(&sh.empty[st]));  // first: behind the other the block may end
     sm100::mma_commit(smem_u32(&sh.o_full[buf]));
-    sm100::mma_commit(smem_u32(&sh.empty[st]));
   }
   __syncwarp();
   return true;
@@ -919,6 +931,8 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
   __nv_bfloat16* o = p.o + grp * G * D;
 
   const int len = p.seq_lens[b];
+  int early = kNone;
+  if (warp == W_LOAD || warp == W_LOAD2) early = early_page(pool, b, C, rank);
   uint4 qraw = make_uint4(0, 0, 0, 0);
   if (tid < NC && (tid >> 4) < G)
     qraw = *reinterpret_cast<const uint4*>(p.q + grp * G * D + tid * 8);
@@ -994,9 +1008,9 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     const bool resident = nt <= 2 * C;
     if (warp == W_LOAD || warp == W_LOAD2) {
       if (resident)
-        ok = load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, own_tile);
+        ok = load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, early, own_tile);
       else
-        ok = load_tiles<false>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, own_tile);
+        ok = load_tiles<false>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, early, own_tile);
     } else if (warp == W_MMA) {
       for (int i = 0; i < tiles && ok; ++i) ok = issue_s<GH>(sh, issuer, resident ? 2 * i : i, i);
     } else if (warp < 4) {
@@ -1093,7 +1107,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
         heads = x >> 24;
       };
       if (ok && !resident)
-        load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, items, done, done, kept_tile);
+        load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, items, done, done, kNone, kept_tile);
     } else if (warp == W_MMA) {
       if (ok) issue_pairs<GH>(sh, issuer, items, done, done, held);
     } else if (warp < 4) {
@@ -1103,7 +1117,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     }
   } else {
     if (warp == W_LOAD || warp == W_LOAD2) {
-      ok = load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, own_tile);
+      ok = load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, tiles, 0u, 0u, early, own_tile);
     } else if (warp == W_MMA) {
       issue_pairs<GH>(sh, issuer, tiles, 0u, 0u, nullptr);
     } else if (warp < 4) {
