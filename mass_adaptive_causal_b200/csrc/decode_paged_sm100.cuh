@@ -23,15 +23,16 @@
 // S[key][.] = K q^T with the K tile as the 128-row operand, O[dim][.] = V^T P with the
 // V tile as the (transposed) 128-row operand. (mma.sync has no e4m3 form of its own here: it
 // is widened to f16, which made a warp's integer work the bound at 45% of the copy
-// bandwidth.) The kernel is bound by HBM: 16 x 131072 tokens of 8 heads, tau = 1: 326 us (2.15 GB
-// of K, the measured copy bandwidth); 16 x 8192, tau = 0: 47 us (5.7 TB/s, 87%); short caches by
-// latency: 1 x 1000: 8.7 us. Two blocks to an SM: while one waits at its ends, the other streams. The other operand is split into four e4m3 terms, 2^4 apart, in columns of
-// their own, and the columns' sums are joined in float32:
+// bandwidth.) The other operand is split into four e4m3 terms, 2^4 apart, in columns of their
+// own, and the columns' sums are joined in float32:
 //  - q, scaled by a power of two per head to have its largest value in [2^7, 2^8): a bf16
 //    value has eight bits, a term carries four, so values within 2^-21 of the largest are
 //    exact, and the rest is off by at most 2^-29 of it;
 //  - P, scaled to 2^8 at the row's reference (its running or final max), is rounded to
 //    f16 and split: exact but for an error of at most 2^-30.
+// The kernel is bound by HBM: 16 x 131072 tokens of 8 heads, tau = 1: 326 us (2.15 GB of K, the
+// measured copy bandwidth); 16 x 8192, tau = 0: 47 us (5.7 TB/s, 87%); short caches by latency:
+// 1 x 1000: 8.7 us. Two blocks to an SM: while one waits at its ends, the other streams.
 // Sums are float32; a row's max and mass never leave float32.
 #pragma once
 
@@ -650,7 +651,8 @@ __device__ __forceinline__ void join_and_store(const Params& p, Shared<GH>& sh,
 #pragma unroll
     for (int g = 0; g < GH; ++g)
       if (g < G)
-        sm100::st_cluster_f32(sm100::mapa_rank(smem_u32(&jn.recv[((int)rank * G + g) * each + i]), owner), out[g]);
+        sm100::st_cluster_f32(
+            sm100::mapa_rank(smem_u32(&jn.recv[((int)rank * G + g) * each + i]), owner), out[g]);
   } else if (tid < NC + C) {
     sm100::st_cluster_u32(sm100::mapa_rank(smem_u32(&jn.bad[rank]), tid - NC), sh.bad);
   }
@@ -723,12 +725,12 @@ struct Walk {
 // A head's bound never falls, so a tile below the bound as it stands now is out for good:
 // the warps sort out, side by side, those that no head could still want at the bound that the
 // newest 32 tiles left, and only the others are looked at one by one (vote and update, about 300
-// cycles each). Group: one warp, a lane per head. Per head: a warp
-// per head.
+// cycles each). Group: one warp, a lane per head. Per head: a warp per head.
 template <int GH>
 __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, unsigned char* smem,
-                                            bool resident, float2* stats, uint32_t* keep, uint32_t* list,
-                                            long long grp, int len, int nt, uint32_t rank) {
+                                            bool resident, float2* stats, uint32_t* keep,
+                                            uint32_t* list, long long grp, int len, int nt,
+                                            uint32_t rank) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.G, GP = p.GP, C = p.C;
   const int units = p.per_head ? G : 1, words = rule_words(p.max_tiles);
@@ -796,8 +798,8 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
         open &= ~(1u << bit);
         const int next = 31 - __clz(open | 1u);
         const float2 y = at[next * GP + seen];  // on its way while this one is decided
-        // nearly every tile that is left is kept: what it would make of the state is worked out beside
-        // the vote, and taken over without a branch
+        // nearly every tile that is left is kept: what it would make of the state is worked out
+        // beside the vote, and taken over without a branch
         Walk kept = w;
         kept.take(x, thr);
         const bool take = __any_sync(0xffffffffu, !(x.x < w.bound));  // a NaN keeps
@@ -1068,7 +1070,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
           for (int q = 0; q < NB; ++q)
             part[q][warp][lane / (32 / GH)] = make_float2(m[q][0], x[q][0]);
         sync_softmax();
-        if (warp < NB && i + warp < tiles && lane < G) {  // the four quarters' statistics as the tile's
+        if (warp < NB && i + warp < tiles && lane < G) {  // the quarters' statistics as the tile's
           float2 y[4];
 #pragma unroll
           for (int w = 0; w < 4; ++w) y[w] = part[warp][w][lane];
@@ -1093,8 +1095,8 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
     }
 
     // ---- B
-    replay_rule<GH>(p, sh, smem + (resident ? 4 * TILE_BYTES : 0), resident, stats, keep, list, grp, len,
-                    nt, rank);
+    replay_rule<GH>(p, sh, smem + (resident ? 4 * TILE_BYTES : 0), resident, stats, keep, list, grp,
+                    len, nt, rank);
 
     // ---- C: values of this block's kept tiles
     const int items = sh.items;
