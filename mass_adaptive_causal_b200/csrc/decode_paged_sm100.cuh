@@ -6,8 +6,8 @@
 //
 // One cluster of C blocks (1 to 16) per (sequence, key/value head), one launch, no
 // workspace; tile t of the sequence is block t mod C's. A block has four warps that do the
-// softmax (a thread per key of a tile, later per dimension of the output), one that looks
-// pages up and loads tiles by TMA into a ring, and one that issues the matrix products.
+// softmax (a thread per key of a tile, later per dimension of the output), two that look
+// pages up and load tiles by TMA into a ring, and one that issues the matrix products.
 //
 // tau > 0 (RULE):
 //  A  scores of every tile, its max m_t and mass l_t per head into the block's shared
