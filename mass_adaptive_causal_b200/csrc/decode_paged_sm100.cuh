@@ -1111,7 +1111,12 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ C
       if (ok && !resident)
         load_tiles<true>(pool, &tmK, &tmV, smem, sh, b, h, len, items, done, done, kNone, kept_tile);
     } else if (warp == W_MMA) {
-      if (ok) issue_pairs<GH>(sh, issuer, items, done, done, held);
+      if (ok) ok = issue_pairs<GH>(sh, issuer, items, done, done, held);
+      // a resident block has asked for the values of all its tiles, and nothing above waits for
+      // those of a skipped one: they must have landed before the block's shared memory goes
+      for (int i = 0; resident && ok && i < tiles; ++i)
+        ok = mbar_wait(smem_u32(&sh.full[2 * i + 1]), 0, &sh.abort, 0x51a);
+      __syncwarp();
     } else if (warp < 4) {
 #pragma unroll
       for (int g = 0; g < GH; ++g) mref[g] = g < G ? sh.mfin[g] : 0.f;

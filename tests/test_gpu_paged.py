@@ -416,6 +416,41 @@ def test_decode_beside_a_prefill_on_another_stream():
     assert all(torch.equal(x, want) for x in outs) and all(torch.equal(x, O) for x in fwd)
 
 
+@pytest.mark.parametrize("B,G", [(148, 4), (8, 4), (148, 8)])
+def test_decode_blocks_that_skip_tiles_whose_values_they_loaded(B, G):
+    """Short caches under a threshold that skips most tiles: a block has asked for the values of
+    all its tiles, and may only end when they are there. Values far from the L2 and a copy that
+    takes the memory's rate make them late; the next blocks use the same shared memory at once."""
+    g = gen(86)
+    Hkv, page, rows = 4, 64, 16
+    lens = [65 + 13 * (b % 40) for b in range(B)]  # up to 5 tiles: one or two to a block
+    base = filled(lens[:40], Hkv, page, "plain", 87, peak=False)
+    n_pages = base[0].shape[0]
+    # the values of `rows` copies of the pool, each used once, and keys that stay in the L2
+    big = [x.view(torch.uint8).repeat(rows, 1, 1, 1).view(f8) for x in base[:2]]
+    scales = [x.repeat(rows, 1) for x in base[2:4]]
+    q = (torch.randn((B, Hkv * G, 128), device="cuda", generator=g) * 0.2).to(bf16)
+    sl = torch.tensor(lens, dtype=i32, device="cuda")
+    t40 = base[4].clamp(0, n_pages - 1)
+    tables = [(t40 + r * n_pages).repeat(4, 1)[:B].contiguous() for r in range(rows)]
+    caches = [mala.PagedCache(*big, *scales, t) for t in tables]
+    want, kept, _ = mala.mala_decode_paged(q, caches[0], sl, tau=1e4, max_seqlen=640, trace=True)
+    torch.cuda.synchronize()
+    tiles = Hkv * sum(-(-n // 128) for n in lens)
+    assert int(kept.sum()) < 0.75 * tiles  # most of the older tiles are skipped
+    noise = torch.empty((2, 1 << 28), dtype=torch.uint8, device="cuda")
+    other = torch.cuda.Stream()
+    outs = []
+    for cache in caches:
+        with torch.cuda.stream(other):
+            noise[1].copy_(noise[0])
+        for _ in range(4):  # blocks of one call follow those of the one before
+            outs.append(mala.mala_decode_paged(q, cache, sl, tau=1e4, max_seqlen=640))
+    torch.cuda.synchronize()
+    mala.mala_check()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 @pytest.mark.parametrize("per_head", [False, True])
 def test_decode_bounds_of_millions_of_tokens(per_head):
     """Short sequences under a table that could hold millions of tokens: the statistics' room
