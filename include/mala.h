@@ -350,6 +350,8 @@ mala_status mala_cache_append(const mala_paged_cache* cache, const void* k,
  * One decode step over the paged cache, with the rule of mala_decode (128-key
  * tiles aligned from position 0, newest first, the newest always kept; Lq =
  * seq_lens[b], which counts the current token; tau = 0 is exact attention).
+ * A tile with a NaN score is kept, and so is every older one (no comparison
+ * with a NaN says "below").
  *
  * Inputs  q: [batch][Hq][d] bf16 contiguous (rotated); seq_lens: [batch] int32.
  * Output  o: [batch][Hq][d] bf16; zero for a sequence of length <= 0; NaN for

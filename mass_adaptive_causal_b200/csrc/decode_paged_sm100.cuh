@@ -722,10 +722,12 @@ struct Walk {
 // fit in the ring's space (a single block's statistics lie in tile order already); leaves the
 // rows' final max and mass, the keep bits, and this block's list of tiles.
 //
-// A head's bound never falls, so a tile below the bound as it stands now is out for good:
-// the warps sort out, side by side, those that no head could still want at the bound that the
-// newest 32 tiles left, and only the others are looked at one by one (vote and update, about 300
-// cycles each). Group: one warp, a lane per head. Per head: a warp per head.
+// A head's bound never falls, so a tile below the bound as it stands now is out for good: the
+// warps sort out, side by side, those that no head could still want at the bound that the newest
+// 32 tiles left, and only the others are looked at one by one (vote and update, about 300
+// cycles each). A NaN score is below no bound and leaves one that nothing is below: its tile is
+// kept, and every older one, sorted out or not. Group: one warp, a lane per head. Per head: a
+// warp per head.
 template <int GH>
 __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, unsigned char* smem,
                                             bool resident, float2* stats, uint32_t* keep,
@@ -795,7 +797,9 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
       int bit = 31 - __clz(open | 1u);
       float2 x = at[bit * GP + seen];
       while (open) {
-        open &= ~(1u << bit);
+        // behind a NaN nothing is below the bound, whatever has been sorted out
+        const bool lost = __any_sync(0xffffffffu, isnan(x.x));
+        open = lost ? (1u << bit) - 1u : open & ~(1u << bit);
         const int next = 31 - __clz(open | 1u);
         const float2 y = at[next * GP + seen];  // on its way while this one is decided
         // nearly every tile that is left is kept: what it would make of the state is worked out
@@ -839,11 +843,19 @@ __device__ __forceinline__ void replay_rule(const Params& p, Shared<GH>& sh, uns
     if (last > first) __syncthreads();
     if (walks)
       for (int w0 = last - 1; w0 >= first; w0 -= 32) {  // 32 words at a time, a lane each
-        const uint32_t mine = w0 - lane >= first ? keep[unit * words + w0 - lane] : 0u;
+        uint32_t done = 0;  // words that need no further look
+        const bool there = w0 - lane >= first;
+        uint32_t mine = there ? keep[unit * words + w0 - lane] : 0u;
         uint32_t some = __ballot_sync(0xffffffffu, mine != 0u);
-        while (some) {
+        while (true) {
+          if (__any_sync(0xffffffffu, isnan(w.bound))) {
+            mine = there ? 0xffffffffu : 0u;
+            some = __ballot_sync(0xffffffffu, mine != 0u) & ~done;
+          }
+          if (!some) break;
           const int src = __ffs(some) - 1;
           some &= some - 1;
+          done = (2u << src) - 1u;
           walk(w0 - src, __shfl_sync(0xffffffffu, mine, src), false);
         }
       }

@@ -354,6 +354,61 @@ def test_decode_a_nan_value_shows_only_in_heads_that_keep_its_tile():
         assert torch.equal(o[0, h, rest], clean[0, h, rest])
 
 
+def rule_with_nan(qn, K, tau, per_head):
+    """The rule read literally, in float64: a tile is skipped only where every head's test says
+    so, and a NaN says nothing of the kind. keep and the tests' margin, [units, nt]"""
+    Hq, Hkv = qn.shape[0], K.shape[0]
+    G, n = Hq // Hkv, K.shape[1]
+    nt = -(-n // 128)
+    units = Hq if per_head else Hkv
+    keep, margin = np.zeros((units, nt), bool), np.full((units, nt), np.inf)
+    thr = math.log(tau) - math.log(n)
+    for u in range(units):
+        heads = [u] if per_head else list(range(u * G, (u + 1) * G))
+        scores = K[heads[0] // G] @ qn[heads].T / math.sqrt(128)
+        lse = np.full(len(heads), -np.inf)
+        for t in range(nt - 1, -1, -1):
+            s = scores[t * 128:(t + 1) * 128]
+            m = s.max(0)
+            if t < nt - 1:
+                margin[u, t] = (m - lse - thr).max()
+                if (m - lse < thr).all():
+                    continue
+            keep[u, t] = True
+            lse = np.log(np.exp(lse - m) + np.exp(s - m).sum(0)) + m
+    return keep, margin
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("nt,Hkv,G,at", [(160, 2, 4, 3), (160, 2, 4, 40), (160, 2, 4, 70),
+                                         (160, 2, 4, 150), (1563, 2, 8, 100), (1563, 2, 8, 1500)])
+def test_decode_a_nan_score_ends_the_skipping(nt, Hkv, G, at, per_head):
+    """One NaN in a tile in the middle of a head's keys: that tile and all older ones are kept,
+    wherever it stands among the words and stretches that the rule is replayed in."""
+    n, page = 128 * nt - 5, 64
+    tensors = filled([n], Hkv, page, "plain", 90 + at, peak=False)
+    k, _, _, _, t = tensors
+    q = (torch.randn((1, Hkv * G, 128), device="cuda", generator=gen(91)) * 0.3).to(bf16)
+    pos = (nt - 1 - at) * 128 + 50
+    k.view(torch.uint8)[int(t[0, pos // page]), 1, pos % page, 7] = 0x7f
+    cache = mala.PagedCache(*tensors)
+    sl = torch.tensor([n], dtype=i32, device="cuda")
+    o, kept, bits = mala.mala_decode_paged(q, cache, sl, tau=300.0, per_head=per_head, trace=True)
+    mala.mala_check()
+    K, _ = R.sequence(tensors[:4], t, 0, n)
+    want, margin = rule_with_nan(as_f64(q)[0], K, 300.0, per_head)
+    got = mala.unpack_bits(bits[0], 32 * bits.shape[2])[:, :nt].astype(bool)
+    assert want[0].mean() < 0.9
+    compared = 0
+    for u in range(want.shape[0]):
+        assert int(kept[0, u]) == got[u].sum()
+        if u >= want.shape[0] // 2:
+            assert got[u, :nt - at].all()
+        compared += not compare_decode_keep(got[u], want[u], margin[u])
+    assert compared >= 0.7 * want.shape[0]
+    assert not torch.isnan(o[0, :G]).any() and torch.isnan(o[0, G:]).all()
+
+
 def test_decode_queries_that_are_not_finite_and_of_all_sizes():
     lens = [500]
     tensors = filled(lens, 1, 16, "plain", 77, peak=False)
