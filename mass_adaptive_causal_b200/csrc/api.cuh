@@ -165,15 +165,14 @@ inline mala_status fwd_bf16(const void* Q, const void* K, const void* V, void* O
   p.nb = (L + fwd2::T - 1) / fwd2::T;
   p.npairs = (p.nb + 1) / 2;
   p.scale_log2 = scale * kLog2e;
-  p.never_skip = tau == 0.f;
   p.log2_tau = tau > 0.f ? log2f(tau) : 0.f;
   p.kept_tiles = kept;
   p.keep_bits = bits;
   p.Hq = Hq;
   p.G = Hq / Hkv;
   // tau = 0 keeps every tile: the instantiation with two P buffers
-  return p.never_skip ? launch_pair<false, true>(mq, mk, mv, p, p.npairs, Z, s)
-                      : launch_pair<false, false>(mq, mk, mv, p, p.npairs, Z, s);
+  return tau == 0.f ? launch_pair<false, true>(mq, mk, mv, p, p.npairs, Z, s)
+                    : launch_pair<false, false>(mq, mk, mv, p, p.npairs, Z, s);
 }
 
 template <bool VARLEN, bool DENSE>
@@ -213,11 +212,7 @@ inline mala_status fwd_varlen_bf16(const void* Q, const void* K, const void* V, 
   p.O = reinterpret_cast<__nv_bfloat16*>(O);
   p.LSE = LSE;
   p.scale_log2 = scale * kLog2e;
-  // tau = 0 goes through the ordinary test with a threshold that every tile
-  // passes: never_skip makes the producer load V ahead of the decisions, which
-  // only the DENSE instantiation's softmax warps count on
-  p.never_skip = 0;
-  p.log2_tau = tau > 0.f ? log2f(tau) : -1e30f;
+  p.log2_tau = tau > 0.f ? log2f(tau) : 0.f;
   p.kept_tiles = kept;
   p.keep_bits = bits;
   p.Hq = Hq;
@@ -227,7 +222,9 @@ inline mala_status fwd_varlen_bf16(const void* Q, const void* K, const void* V, 
   p.total_q = total_q;
   p.nbq_max = (max_q + fwd2::T - 1) / fwd2::T;
   p.nw = varlen_trace_words(max_q, max_k);
-  return launch_pair<true, false>(mq, mk, mv, p, (p.nbq_max + 1) / 2, batch * Hq, s);
+  const int npairs = (p.nbq_max + 1) / 2, Z = batch * Hq;
+  return tau == 0.f ? launch_pair<true, true>(mq, mk, mv, p, npairs, Z, s)
+                    : launch_pair<true, false>(mq, mk, mv, p, npairs, Z, s);
 }
 
 // ---------------------------------------------------------------- backward

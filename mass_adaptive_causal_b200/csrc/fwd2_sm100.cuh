@@ -137,8 +137,7 @@ struct Params {
   int nb;      // query / key blocks
   int npairs;  // ceil(nb / 2)
   float scale_log2;
-  float log2_tau;
-  int never_skip;
+  float log2_tau;  // not used where DENSE
   int32_t* kept_tiles;
   uint32_t* keep_bits;
   int Hq, G;  // query heads; G query heads share each key/value head
@@ -341,6 +340,7 @@ struct KeepBitsOr {
   }
 };
 
+// DENSE: tau = 0, every legal tile is kept.
 template <bool VARLEN, bool DENSE>
 __global__ void __launch_bounds__(NT, 1)
     fwd_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(NT, 1)
   // PVs whose V the producer loads without a request: the diagonal tiles,
   // always kept and the first PVs (t = 0 for rank 1's block, t = 1 for rank
   // 0's), or every tile when nothing is skipped.
-  const int npre = p.never_skip ? ntiles : (hasB ? 2 : 1);
+  const int npre = DENSE ? ntiles : min(2, nb - i0);
   // S buffer barrier pair member of tile t
   auto sg = [&](int t) { return t & PL::SGRP_MASK; };
 
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(NT, 1)
     // (packed chunks: a row past the packed tensor is never written, whatever
     // the offsets say)
     const bool row_valid = mine && row < Lq && (!VARLEN || yq0 + row < p.total_q);
-    const float thr = p.never_skip ? 0.f : (p.log2_tau - __log2f((float)(off + row + 1)));
+    const float thr = p.log2_tau - __log2f((float)(off + row + 1));
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lane_base + TMEM_O;
     auto signal = [&](int t, int keep) {  // one thread: this CTA's decision for tile t
