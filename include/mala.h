@@ -362,7 +362,7 @@ mala_status mala_cache_append(const mala_paged_cache* cache, const void* k,
  *         ceil(max_seqlen / 128); with per_head = 1, [batch][Hq] and
  *         [batch][Hq][ceil(nt/32)].
  * Precision: q and the probabilities enter the e4m3 products as four e4m3 terms
- * each. A probability is rounded to f16, and below that to 2^-30 of the row's
+ * each. A probability is off by at most 2^-16 of itself or 2^-30 of the row's
  * largest; where a 128-key tile has pages of different value scales, both count
  * relative to the largest of them. Sums, maxima and masses are float32.
  * No workspace. Supported: 1 <= Hq / Hkv <= 8, batch, Hkv <= 65535;

@@ -28,8 +28,9 @@
 //  - q, scaled by a power of two per head to have its largest value in [2^7, 2^8): a bf16
 //    value has eight bits, a term carries four, so values within 2^-21 of the largest are
 //    exact, and the rest is off by at most 2^-29 of it;
-//  - P, scaled to 2^8 at the row's reference (its running or final max), is rounded to
-//    f16 and split: exact but for an error of at most 2^-30.
+//  - P, scaled to 2^8 at the row's reference (its running or final max), is split from float32,
+//    what its first term leaves going on in f16: off by at most 2^-16 of itself, or 2^-30 of
+//    the reference.
 // The kernel is bound by HBM: 16 x 131072 tokens of 8 heads, tau = 1: 326 us (2.15 GB of K, the
 // measured copy bandwidth); 16 x 8192, tau = 0: 47 us (5.7 TB/s, 87%); short caches by latency:
 // 1 x 1000: 8.7 us. Two blocks to an SM: while one waits at its ends, the other streams.
@@ -287,19 +288,23 @@ __device__ __forceinline__ void join_terms(const uint32_t (&v)[TERMS * GH], floa
   }
 }
 
-// A key's probabilities (scaled by 2^8) as e4m3 terms into its row of P.
+// A key's probabilities (scaled by 2^8) as e4m3 terms into its row of P. The first term is taken
+// from float32; what it leaves is at most 2^-4 of the value, and goes on in f16, rounded by 2^-12
+// of itself.
 template <int GH>
 __device__ __forceinline__ void store_p(unsigned char* buf, int key, const float (&p)[GH]) {
   uint32_t w[TERMS][GH / 4];
   const __half2 up = __float2half2_rn(16.f), down = __float2half2_rn(-16.f);
 #pragma unroll
   for (int j = 0; j < GH / 2; ++j) {
-    __half2 h = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
+    uint32_t t = paged::floats_to_e4m3x2(p[2 * j], p[2 * j + 1]);
+    const float2 f = __half22float2(e4m3x2_to_half2(t));
+    __half2 h = __hmul2(__floats2half2_rn(p[2 * j] - f.x, p[2 * j + 1] - f.y), up);
 #pragma unroll
     for (int k = 0; k < TERMS; ++k) {
-      const uint32_t t = f16x2_to_e4m3x2(h);
+      if (k > 0) t = f16x2_to_e4m3x2(h);
       w[k][j / 2] = (j & 1) ? w[k][j / 2] | t << 16 : t;
-      if (k + 1 < TERMS) h = __hfma2(e4m3x2_to_half2(t), down, __hmul2(h, up));
+      if (k > 0 && k + 1 < TERMS) h = __hfma2(e4m3x2_to_half2(t), down, __hmul2(h, up));
     }
   }
   const uint32_t* x = &w[0][0];

@@ -432,6 +432,46 @@ def test_decode_queries_that_are_not_finite_and_of_all_sizes():
         assert (np.abs(on[0, h] - ref) <= tol).all(), h
 
 
+@pytest.mark.parametrize("tau", [0.0, 1.0])
+@pytest.mark.parametrize("G", [4, 7])
+def test_decode_probabilities_hold_sixteen_bits(G, tau):
+    """Keys in pairs whose values cancel: an output is the difference of two probabilities near
+    each other, far below their sum, so that its own rounding hides nothing of theirs.
+
+    The bound of tests/paged_ref.py with 2^-16 in the place of 2^-11: a probability p in [2^e,
+    2^(e+1)) goes in as four e4m3 terms; the first leaves at most half its step, 2^(e-4), which goes
+    on rounded to f16, by at most 2^-12 of itself; the other three hold those eleven bits (four
+    and a sign each), down to 2^-30 of the row's largest. Scores of about 2^-8, so that their own
+    part of the bound, 4 * 129 * 2^-23 A, is below 2^-16."""
+    B, Hkv, page, n = 64, 2, 16, 2
+    g = gen(88)
+    k, v, ks, vs = new_pool(B, Hkv, page)
+    x = torch.randn((B, Hkv, 2, 128), device="cuda", generator=g).clamp(-4, 4)
+    y = torch.randn((B, Hkv, 1, 128), device="cuda", generator=g).clamp(-4, 4)
+    k.view(torch.uint8)[:, :, :2] = (100 * x).to(f8).view(torch.uint8)
+    v.view(torch.uint8)[:, :, :2] = (100 * torch.cat([y, -y], 2)).to(f8).view(torch.uint8)
+    ks[:], vs[:] = 2.0 ** -7, 2.0 ** -7
+    t = torch.arange(B, dtype=i32, device="cuda")[:, None]
+    q = (torch.randn((B, Hkv * G, 128), device="cuda", generator=g) * 0.004).to(bf16)
+    cache = mala.PagedCache(k, v, ks, vs, t)
+    o = mala.mala_decode_paged(q, cache, torch.full((B,), n, dtype=i32, device="cuda"), tau=tau)
+    mala.mala_check()
+    qn, on = as_f64(q), as_f64(o)
+    for b in range(B):
+        K, V = R.sequence((k, v, ks, vs), t, b, n)
+        for h in range(Hkv * G):
+            kk, vv = K[h // G], V[h // G]
+            s = kk @ qn[b, h] / math.sqrt(128)
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            ref, S = p @ vv, p @ np.abs(vv)
+            A = (np.abs(kk) @ np.abs(qn[b, h])).max() / math.sqrt(128)
+            rest = 2.0 ** -29 * np.abs(qn[b, h]).max() * np.abs(kk).sum(-1).max() / math.sqrt(128)
+            tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -30 * p.max() * np.abs(vv).sum(0) \
+                + S * (2.0 ** -16 + 4 * (129 * 2.0 ** -23 * A + rest) + 2.0 ** -20)
+            assert (np.abs(on[b, h] - ref) <= tol).all(), (b, h)
+
+
 @pytest.mark.parametrize("page", [16, 64])
 def test_decode_pages_of_very_different_scales(page):
     lens = [700, 130]
