@@ -95,15 +95,17 @@ inline int decode_cluster(const pdec::Params& p, long long groups, bool rule, si
   return best;
 }
 
-// What a decode kernel may use, said once per device: three calls of the runtime for
-// each step would be a tenth of its host time.
+// What a decode kernel may use, said once per device and context: three calls of the runtime for
+// each step would be a tenth of its host time. Remembered is the context that it was said in: after
+// cudaDeviceReset it has to be said again, or the launch is refused.
 inline bool allow_decode(pdec::Kernel kernel, bool wide, bool rule) {
-  static std::atomic<unsigned long long> said[2][2];
+  constexpr int kDevices = 64;
+  static std::atomic<unsigned long long> said[2][2][kDevices];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  std::atomic<unsigned long long>& mine = said[wide][rule];
-  if (mine.load(std::memory_order_relaxed) & bit) return true;
+  unsigned long long ctx = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || !current_context_id(&ctx)) return false;
+  std::atomic<unsigned long long>* mine = dev < kDevices ? &said[wide][rule][dev] : nullptr;
+  if (mine && ctx != 0 && mine->load(std::memory_order_relaxed) == ctx) return true;
   // the carve-out: without it an SM takes one block, although the shared memory of two fits
   const bool ok =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -112,7 +114,7 @@ inline bool allow_decode(pdec::Kernel kernel, bool wide, bool rule) {
           cudaSuccess &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                            cudaSharedmemCarveoutMaxShared) == cudaSuccess;
-  if (ok) mine.fetch_or(bit, std::memory_order_relaxed);
+  if (ok && mine && ctx != 0) mine->store(ctx, std::memory_order_relaxed);
   return ok;
 }
 

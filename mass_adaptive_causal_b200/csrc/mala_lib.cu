@@ -28,30 +28,6 @@ struct ScratchSlot {
 };
 ScratchSlot g_scratch[kMaxDevices];
 
-using CtxGetCurrentFn = CUresult (*)(CUcontext*);
-using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long*);
-
-template <typename Fn>
-Fn driver_fn(const char* name) {
-  void* ptr = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPoint(name, &ptr, cudaEnableDefault, &q) != cudaSuccess ||
-      q != cudaDriverEntryPointSuccess)
-    return nullptr;
-  return reinterpret_cast<Fn>(ptr);
-}
-
-// The unique ID of the context current on this thread (0 if none yet).
-bool current_context_id(unsigned long long* id) {
-  static const CtxGetCurrentFn get_current = driver_fn<CtxGetCurrentFn>("cuCtxGetCurrent");
-  static const CtxGetIdFn get_id = driver_fn<CtxGetIdFn>("cuCtxGetId");
-  if (!get_current || !get_id) return false;
-  CUcontext ctx = nullptr;
-  if (get_current(&ctx) != CUDA_SUCCESS) return false;
-  *id = 0;
-  return !ctx || get_id(ctx, id) == CUDA_SUCCESS;
-}
-
 // In host code `g_decode_scratch` only names the array; its address on the
 // current device comes from the runtime, once per device and context, and is
 // cached.
@@ -59,7 +35,7 @@ mala_status scratch_on_current_device(unsigned char** out) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MALA_ERR_CUDA;
   unsigned long long id = 0;
-  if (!current_context_id(&id)) return MALA_ERR_CUDA;
+  if (!mala::host::current_context_id(&id)) return MALA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_scratch_mutex);
   ScratchSlot& slot = g_scratch[dev];
   if (id == 0 || slot.ptr == nullptr || slot.ctx_id != id) {
@@ -67,7 +43,7 @@ mala_status scratch_on_current_device(unsigned char** out) {
     unsigned char* ptr = nullptr;
     if (cudaGetSymbolAddress((void**)&ptr, g_decode_scratch) != cudaSuccess || !ptr)
       return MALA_ERR_CUDA;
-    if (id == 0 && (!current_context_id(&id) || id == 0)) return MALA_ERR_CUDA;
+    if (id == 0 && (!mala::host::current_context_id(&id) || id == 0)) return MALA_ERR_CUDA;
     slot.ptr = ptr;
     slot.ctx_id = id;
   }
