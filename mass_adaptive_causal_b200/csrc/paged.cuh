@@ -8,9 +8,12 @@
 // powers of two: e4m3 is itself a floating-point format, so a scale's mantissa
 // would buy no precision, while with powers of two
 //  - a later, larger token of the page only adds to the exponent, and the
-//    earlier tokens are re-rounded without loss (but for values that fall among
-//    e4m3's subnormals: an error of at most 2^-10 of the new scale);
-//  - the cache's content does not depend on how its tokens came in;
+//    earlier tokens are re-rounded without loss, but for values that sink among
+//    e4m3's subnormals, 2^-9 of the scale apart: each growth rounds those by at
+//    most 2^-10 of the scale it leads to, all growths by less than 2^-9 of the
+//    last one (the scales at least double);
+//  - so the cache's content does not depend on how its tokens came in, but for
+//    such values, which may come out one subnormal step apart;
 //  - a dequantized value is exact in bf16.
 #pragma once
 

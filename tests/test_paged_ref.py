@@ -58,3 +58,35 @@ def test_a_prompt_at_once_or_token_by_token_gives_one_cache():
     for w in range(2):
         assert np.array_equal(one.scale[w], many.scale[w])
         assert np.array_equal(one.val[w], many.val[w])
+
+
+def test_rounding_again_as_a_scale_grows_stays_within_a_step():
+    """Tokens one by one, each larger than those before, so that a page's scale grows again and
+    again and earlier values sink among e4m3's subnormals, 2^-9 of the scale apart. A value is
+    rounded once more at each growth, by at most 2^-10 of the scale it goes to; the scales at
+    least double, so the sum is below 2^-9 of the last one (a first rounding while the value was
+    normal, 2^-4 of a power of two below 2^-6 of the scale s at which it first is not, is below
+    2^-11 s and does not change that). Rounding at once is off by at most 2^-10 of it, so the two
+    are at most one subnormal step apart. Normal values are the same either way."""
+    rng = np.random.default_rng(6)
+    n = 16
+    x = rng.standard_normal((n, 2, 128)) * np.exp2(np.linspace(-9, 9, n))[:, None, None] \
+        * rng.choice([1, 2.0 ** -4, 2.0 ** -8], (n, 2, 128))
+    x = torch.tensor(x).bfloat16()
+    empty = lambda: (torch.zeros((1, 2, 16, 128), dtype=torch.uint8),) * 2 + \
+        (torch.ones(1, 2),) * 2 + (torch.tensor([[0]]),)  # noqa: E731
+    one, many = R.RefCache(*empty()), R.RefCache(*empty())
+    one.append(x, x, [n], [0, n])
+    for i in range(n):
+        many.append(x[i:i + 1], x[i:i + 1], [i + 1])
+    s = one.scale[0][0]
+    assert np.array_equal(s, many.scale[0][0])
+    exact = x.double().numpy().transpose(1, 0, 2) / s[:, None, None]
+    a, b = one.val[0][0], many.val[0][0]
+    small = (np.abs(a) <= 2.0 ** -6) & (np.abs(b) <= 2.0 ** -6)
+    assert np.array_equal(a[~small], b[~small])
+    assert (np.abs(b - exact)[small] < 2.0 ** -9).all() and (np.abs(a - b)[small] <= 2.0 ** -9).all()
+    assert (a != b).any()
+    # rounded at scale 1, then again at scale 4
+    first = R.round_e4m3(0.058349609375)
+    assert R.round_e4m3(first / 4) * 4 == 0.0625 and R.round_e4m3(0.058349609375 / 4) * 4 == 0.0546875
