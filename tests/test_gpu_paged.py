@@ -623,6 +623,61 @@ def test_append_prompts_chunks_and_steps(page, layout, rot, inter):
         assert (q_out[torch.tensor(np.isnan(want[:, 0, 0]))] == 777.0).all()
 
 
+@pytest.mark.parametrize("page,B,total,Hkv,G,rot,inter,in_place", [
+    (16, 24, 480, 8, 4, 64, False, True),    # all eight heads to a block, rows of one warp
+    (16, 10, 400, 8, 8, 32, True, False),    # 3 + 3 + 2 heads
+    (32, 30, 700, 7, 5, 96, False, False),   # seven heads and 35 queries' heads, more than 32
+    (64, 40, 1000, 8, 8, 32, False, True),   # two warps to a row group; 64 queries' heads
+    (64, 24, 900, 5, 3, 32, True, True),     # 3 + 2 heads
+    (128, 50, 1500, 8, 2, 32, False, False),  # four warps
+    (128, 28, 1400, 3, 8, 16, True, True),   # 2 + 1 heads
+    (128, 50, 1500, 8, 0, 32, True, False),  # no queries
+])
+def test_append_blocks_of_several_heads(page, B, total, Hkv, G, rot, inter, in_place):
+    """Calls whose (page, sequence) blocks would fill the chip, so that a block takes several heads
+    one after the other: the next unit's rows come while the last one's are stored, the page's
+    maxima go through the same shared memory again, and the last block of a page may have fewer
+    heads. A chunk of small tokens, then one of large ones behind it (scales grow in the middle of
+    pages), runs of 0 to 2 pages; the bound of the new tokens is that of all sequences together."""
+    g = gen(1000 * page + Hkv)
+    rng = np.random.default_rng(page + Hkv)
+    Hq = G * Hkv
+    chunks = []
+    for _ in range(2):
+        news = rng.choice([0, 1, 5, page - 1, page, page + 3, 2 * page + 1], B)
+        while news.sum() > total:
+            news[rng.integers(B)] //= 2
+        chunks.append(news.tolist())
+    final = np.sum(chunks, 0).tolist()
+    n_pages = pages_needed(final, page) + 2
+    k_pages, v_pages, ks, vs = new_pool(n_pages, Hkv, page, "token_major")
+    t = table_for(final, page, n_pages, g)
+    cache = mala.PagedCache(k_pages, v_pages, ks, vs, t)
+    freq = (1e4 ** (-torch.arange(rot // 2, device="cuda") / (rot // 2))).float()
+    lens = [0] * B
+    for news, size in zip(chunks, (0.05, 2.0)):
+        lens = [a + b for a, b in zip(lens, news)]
+        cu = np.concatenate([[0], np.cumsum(news)]).tolist()
+        q, k, v = projection(total, Hq, Hkv, g, size)
+        given = q.clone()
+        # from the cache as it lies there: what an earlier chunk left next to a tie may have fallen
+        # on either side of it, and is now rounded again from there
+        ref = R.RefCache(k_pages, v_pages, ks, vs, t)
+        out = None
+        if G:
+            out = q if in_place else torch.full((total, Hq, 128), 777.0, dtype=bf16, device="cuda")
+        mala.mala_cache_append(cache, k, v, torch.tensor(lens, dtype=i32, device="cuda"),
+                               cu_seqlens=torch.tensor(cu, dtype=i32, device="cuda"), inv_freq=freq,
+                               interleaved=inter, q=q if G else None, q_out=out)
+        mala.mala_check()
+        want, tol = ref.append(k, v, lens, cu, freq, inter, given if G else None)
+        ref.check(k_pages, v_pages, ks, vs)
+        if G:
+            check_q(out, want, tol)
+            rest = torch.tensor(np.isnan(want[:, 0, 0]))
+            assert torch.equal(out[rest], given[rest] if in_place else torch.full_like(given[rest], 777))
+
+
 def test_append_scales_grow_and_hold():
     """Tokens of growing, shrinking, zero, tiny, huge and non-finite values into one page."""
     page = 32
