@@ -535,6 +535,16 @@ def _check_batch(cache, batch):
                          f"{cache.sequences} rows")
 
 
+def _check_bound(x, name):
+    """An upper bound that the library takes as an int (beyond 32 bits it would wrap)."""
+    x = int(x)
+    if x < 0:
+        raise ValueError(f"{name} must not be negative")
+    if x > 0x7fffffff:
+        raise ValueError(f"{name} must be below 2**31")
+    return x
+
+
 def _rows(torch, cache, t, name, total, heads):
     """bf16 [total, heads, 128] with rows that may lie apart (None: any number of them):
     (pointer, token stride, head stride, total, heads)."""
@@ -582,9 +592,7 @@ def mala_cache_append(cache, k, v, seq_lens, cu_seqlens=None, max_new: int | Non
         max_new = 1
     else:
         cu, _ = _check_lens(torch, cache, cu_seqlens, "cu_seqlens", batch + 1)
-        max_new = total if max_new is None else int(max_new)
-        if max_new < 0:
-            raise ValueError("max_new must not be negative")
+        max_new = total if max_new is None else _check_bound(max_new, "max_new")
     vp, vt, vh, _, _ = _rows(torch, cache, v, "v", total, cache.Hkv)
     qp = op = None
     qt = qh = ot = oh = Hq = 0
@@ -640,9 +648,12 @@ def mala_decode_paged(q, cache, seq_lens, tau: float = 1.0, scale: float = 0.0,
     if Hq < 1 or Hq % cache.Hkv:
         raise ValueError("the query heads must be a multiple of the key/value heads")
     lens, _ = _check_lens(torch, cache, seq_lens, "seq_lens", batch)
-    limit = cache.max_seqlen if max_seqlen is None else int(max_seqlen)
-    if limit < 1:
-        raise ValueError("max_seqlen must be positive")
+    limit = cache.max_seqlen
+    if max_seqlen is not None:
+        limit = int(max_seqlen)
+        if limit < 1:
+            raise ValueError("max_seqlen must be positive")
+        _check_bound(limit, "max_seqlen")
     o = torch.empty_like(q) if out is None else _buf(out, "out", cache._device, q.dtype, shape)
     kept = bits = None
     if trace:
@@ -666,9 +677,7 @@ def mala_cache_gather(cache, cu_seqlens_k, max_seqlen: int, total: int, out=None
     cu, entries = _check_lens(torch, cache, cu_seqlens_k, "cu_seqlens_k")
     batch = entries - 1
     _check_batch(cache, batch)
-    total, max_seqlen = int(total), int(max_seqlen)
-    if total < 0 or max_seqlen < 0:
-        raise ValueError("total and max_seqlen must not be negative")
+    total, max_seqlen = _check_bound(total, "total"), _check_bound(max_seqlen, "max_seqlen")
     if out is None:
         k = cache._tensors[2].new_empty((total, cache.Hkv, 128), dtype=torch.bfloat16)
         v = torch.empty_like(k)

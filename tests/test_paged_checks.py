@@ -183,6 +183,23 @@ def test_gather_marshals_and_refuses(rec):
     assert len(rec.calls) == n
 
 
+def test_bounds_beyond_32_bits_are_refused(rec):
+    """They would wrap on their way into the library: 2**32 + 100 into a bound of 100."""
+    c = make()
+    q, kv = torch.zeros((3, 4, 128), dtype=bf16), torch.zeros((3, 2, 128), dtype=bf16)
+    lens, cu = torch.ones(3, dtype=i32), torch.tensor([0, 1, 2, 3], dtype=i32)
+    for big in (2 ** 31, 2 ** 32 + 100, 2 ** 63):
+        for call in (lambda: mala.mala_decode_paged(q, c, lens, max_seqlen=big),
+                     lambda: mala.mala_cache_append(c, kv, kv, lens, cu_seqlens=cu, max_new=big),
+                     lambda: mala.mala_cache_gather(c, cu, big, 3),
+                     lambda: mala.mala_cache_gather(c, cu, 3, big)):
+            with pytest.raises(ValueError, match="2\\*\\*31"):
+                call()
+    assert not rec.calls
+    mala.mala_decode_paged(q, c, lens, max_seqlen=2 ** 31 - 1)
+    assert rec.calls[-1][1][6] == 2 ** 31 - 1
+
+
 # ------------------------------------------------------------------ the C entry points
 def struct(**kw):
     f = dict(k_pages=256, v_pages=256, k_scale=256, v_scale=256, page_table=256,
