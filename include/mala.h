@@ -327,8 +327,10 @@ typedef struct {
  *         token and head strides (in elements, multiples of 8; d contiguous;
  *         base pointers 16-byte aligned), so that rows of a fused projection can
  *         be passed as they lie; inv_freq: float32 [rot_dim / 2].
- * Outputs the cache; q_out: [total][Hq][d] bf16 by its strides (may be q itself).
- * max_new >= every n_b.
+ * Outputs the cache; q_out: [total][Hq][d] bf16 by its strides (may be q itself;
+ *         overlaps no other input, and q not otherwise).
+ * max_new >= every n_b. The launch has a block for every page that max_new
+ * tokens could reach in every sequence; those without tokens leave at once.
  * A sequence with n_b > max_new, with rows outside [0, total) or with 0 <
  * seq_lens[b] < n_b is left untouched, tokens whose page is not in the pool
  * are left out (both reported); a sequence of length <= 0 (an unused slot of

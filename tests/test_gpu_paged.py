@@ -678,6 +678,44 @@ def test_append_blocks_of_several_heads(page, B, total, Hkv, G, rot, inter, in_p
             assert torch.equal(out[rest], given[rest] if in_place else torch.full_like(given[rest], 777))
 
 
+@pytest.mark.parametrize("B,Hkv,G,rot,inter,in_place", [
+    (20, 8, 4, 128, False, True), (20, 8, 8, 64, True, False), (7, 40, 0, 128, True, False),
+    (33, 5, 3, 0, False, True), (3, 1, 1, 96, False, False)])
+def test_append_up_to_two_tokens_each(B, Hkv, G, rot, inter, in_place):
+    """A draft token beside the newest one: none, one or two new tokens, within a page and across
+    its end, growing and shrinking, in blocks of some of the heads."""
+    g = gen(B + Hkv)
+    page, Hq = 16, G * Hkv
+    lens = [int(x) for x in np.random.default_rng(B).integers(0, 3 * page, B)]
+    lens[0], lens[1], lens[2] = page - 1, page, 0
+    n_pages = pages_needed([n + 10 for n in lens], page)
+    k_pages, v_pages, ks, vs = new_pool(n_pages, Hkv, page, "interleaved_kv")
+    t = table_for([n + 10 for n in lens], page, n_pages, g)
+    cache = mala.PagedCache(k_pages, v_pages, ks, vs, t)
+    freq = (1e4 ** (-torch.arange(rot // 2, device="cuda") / (rot // 2 or 1))).float() if rot else None
+    _, k, v = projection(max(sum(lens), 1), 0, Hkv, g)
+    mala.mala_cache_append(cache, k, v, torch.tensor(lens, dtype=i32, device="cuda"), inv_freq=freq,
+                           cu_seqlens=torch.tensor([0, *np.cumsum(lens)], dtype=i32, device="cuda"),
+                           interleaved=inter)
+    for step, size in enumerate((0.3, 6.0, 1.0)):
+        news = [(b + step) % 3 for b in range(B)]
+        lens = [a + b for a, b in zip(lens, news)]
+        cu = np.concatenate([[0], np.cumsum(news)]).tolist()
+        T = cu[-1]
+        q, k, v = projection(T, Hq, Hkv, g, size)
+        given = q.clone()
+        ref = R.RefCache(k_pages, v_pages, ks, vs, t)
+        out = mala.mala_cache_append(cache, k, v, torch.tensor(lens, dtype=i32, device="cuda"),
+                                     cu_seqlens=torch.tensor(cu, dtype=i32, device="cuda"), max_new=2,
+                                     inv_freq=freq, interleaved=inter, q=q if G else None,
+                                     q_out=q if G and in_place else None)
+        mala.mala_check()
+        want, tol = ref.append(k, v, lens, cu, freq, inter, given if G else None)
+        ref.check(k_pages, v_pages, ks, vs)
+        if G:
+            check_q(out, want, tol)
+
+
 def test_append_scales_grow_and_hold():
     """Tokens of growing, shrinking, zero, tiny, huge and non-finite values into one page."""
     page = 32
