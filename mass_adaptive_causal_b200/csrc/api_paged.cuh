@@ -77,10 +77,18 @@ inline bool make_page_map(CUtensorMap* m, const void* base, const paged::Pool& p
 
 // Blocks of a decode cluster: the largest power of two that leaves no more than 1.3 waves of
 // blocks (two to an SM), 0 when the statistics of the longest sequence do not fit. More splits a
-// long sequence finer but adds blocks that cost 8 us each and run in a second wave: 16 x 8 heads
-// x 8192 keys, exact: 2 blocks 48 us, 4: 57 us; 24 x 8 heads ragged to 16384: 1 block 83 us, 2: 39 us,
-// 4: 51 us. Clusters of 16 blocks do not pack: the chip holds 14, not 18, so they are for
-// fewer groups than that (16 groups of 16384 keys: 8 blocks 41 us, 16: 59 us).
+// long sequence finer but adds blocks that cost 8 us each and run in a second wave. The host knows
+// how many sequences there are, not how long each is, and the best size depends on both; the rule
+// favours ragged batches, whose short sequences leave the second wave room. In us, the chosen size
+// first, groups = sequences x 8 heads:
+//   24 ragged to 16384 (192 groups), tau = 1 (and 0): 2 blocks 39 (60), 1: 59 (106), 4: 45 (43)
+//   uniform, 8192 keys, tau = 0:  40 groups: 8 blocks 27, 4: 24, 16: 33;  80: 4 blocks 44, 2: 39,
+//     8: 43;  128: 2 blocks 47, 4: 57;  160: 2 blocks 78, 1: 67, 4: 70;  192: 2 blocks 80, 1: 71;
+//     256: 1 block 83;  320: 1 block 141 (24 blocks run a second wave alone), 2: 125, 4: 121;
+//     384: 1 block 147, 2: 132;  512: 1 block 161
+// So a uniform batch just above a whole wave pays up to 1.2 times for what a ragged one gains.
+// Clusters of 16 blocks do not pack: the chip holds 14, not 18, so they are for fewer groups than
+// that (16 groups of 16384 keys: 8 blocks 41 us, 16: 59 us).
 inline int decode_cluster(const pdec::Params& p, long long groups, bool rule, size_t* smem) {
   int best = 0;
   for (int C = 1; C <= pdec::MAXC; C *= 2) {

@@ -225,7 +225,8 @@ __device__ __forceinline__ void rescale16(uint8_t* p, float ratio) {
 // memory for all heads of the block. 4 x 8192 tokens of 8 + 32 heads, pages of 128: 143 us (5.2 TB/s,
 // 79% of the measured copy bandwidth; 48% of the issue slots with sixteen warps an SM, without
 // rotation 124 us). Four rows a thread and 256 threads a unit, three blocks to an SM instead of
-// two: 183 us. 256 single tokens: 7.7 us, latency.
+// two: 183 us. 256 single tokens: 7.7 us, latency (where no scale grows; 16 us where 40% do, their
+// earlier rows read and written by a warp for its four units in turn).
 template <int LPU, int PASSES, bool INTERLEAVED>
 __global__ void __launch_bounds__(APPEND_NT, 2) append_kernel(const AppendParams p) {
   constexpr int UNITS = APPEND_NT / LPU;  // side by side
