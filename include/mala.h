@@ -320,7 +320,8 @@ typedef struct {
  * e4m3's subnormals are off by less than 2^-9 of the last scale after all such
  * roundings; the others lose nothing). Stored is e4m3(x / s), to nearest even
  * (x times the float32 reciprocal of s, the same for powers of two); infinities
- * and NaN are stored as NaN. Values likewise. Rows of the page behind the new tokens are left as they were.
+ * and NaN are stored as NaN. Values likewise. Rows of the page behind the new
+ * tokens are left as they were.
  * (The cache's scales are powers of two as long as only this call writes them.)
  *
  * Inputs  k, v: [total][Hkv][d] bf16, q: [total][Hq][d] bf16 or NULL, by their

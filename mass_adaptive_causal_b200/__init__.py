@@ -580,8 +580,8 @@ def mala_cache_append(cache, k, v, seq_lens, cu_seqlens=None, max_new: int | Non
     bound of the new tokens of a sequence (default total, or 1; the launch has a block for every
     page that so many tokens could reach in every sequence, so a close one is faster);
     inv_freq: float32 [rot_dim / 2], rot_dim a multiple of 16 (None: no rotation); interleaved:
-    pairs (2i, 2i+1) instead of (i, i + rot_dim / 2). Returns q rotated (q_out, which may be q but must not
-    overlap it otherwise, nor k or v; a new tensor if None), or None without q."""
+    pairs (2i, 2i+1) instead of (i, i + rot_dim / 2). Returns q rotated (q_out, which may be q but
+    must not overlap it otherwise, nor k or v; a new tensor if None), or None without q."""
     torch = _paged_ready(cache)
     lens, batch = _check_lens(torch, cache, seq_lens, "seq_lens")
     _check_batch(cache, batch)

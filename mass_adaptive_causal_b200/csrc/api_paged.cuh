@@ -86,8 +86,10 @@ inline bool make_page_map(CUtensorMap* m, const void* base, const paged::Pool& p
 //     8: 43;  128: 2 blocks 47, 4: 57;  160: 2 blocks 78, 1: 67, 4: 70;  192: 2 blocks 80, 1: 71;
 //     256: 1 block 83;  320: 1 block 141 (24 blocks run a second wave alone), 2: 125, 4: 121;
 //     384: 1 block 147, 2: 132;  512: 1 block 161
-// So a uniform batch just above a whole wave pays up to 1.2 times for what a ragged one gains.
-// Clusters of 16 blocks do not pack: the chip holds 14, not 18, so they are for fewer groups than
+//   and tau = 1:  40: 8 blocks 29, 4: 20;  80: 4 blocks 42, 2: 31;  160: 2 blocks 65, 1: 52;  192:
+//     2 blocks 68, 1: 57;  320: 1 block 109, 2: 105
+// So a uniform batch just above a whole wave pays up to 1.2 times (tau = 1: 1.4) for what a ragged
+// one gains. Clusters of 16 blocks do not pack: the chip holds 14, not 18, so they are for fewer groups than
 // that (16 groups of 16384 keys: 8 blocks 41 us, 16: 59 us).
 inline int decode_cluster(const pdec::Params& p, long long groups, bool rule, size_t* smem) {
   int best = 0;

@@ -289,8 +289,8 @@ __device__ __forceinline__ void join_terms(const uint32_t (&v)[TERMS * GH], floa
 }
 
 // A key's probabilities (scaled by 2^8) as e4m3 terms into its row of P. The first term is taken
-// from float32; what it leaves is at most 2^-4 of the value, and goes on in f16, rounded by 2^-12
-// of itself.
+// from float32; what it leaves of a value in [2^e, 2^(e+1)) is at most 2^(e-4), and goes on in f16,
+// rounded by at most 2^(e-16).
 template <int GH>
 __device__ __forceinline__ void store_p(unsigned char* buf, int key, const float (&p)[GH]) {
   uint32_t w[TERMS][GH / 4];

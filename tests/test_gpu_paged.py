@@ -440,7 +440,7 @@ def test_decode_probabilities_hold_sixteen_bits(G, tau):
 
     The bound of tests/paged_ref.py with 2^-16 in the place of 2^-11: a probability p in [2^e,
     2^(e+1)) goes in as four e4m3 terms; the first leaves at most half its step, 2^(e-4), which goes
-    on rounded to f16, by at most 2^-12 of itself; the other three hold those eleven bits (four
+    on rounded to f16, by at most 2^(e-16); the other three hold those eleven bits (four
     and a sign each), down to 2^-30 of the row's largest. Scores of about 2^-8, so that their own
     part of the bound, 4 * 129 * 2^-23 A, is below 2^-16."""
     B, Hkv, page, n = 64, 2, 16, 2
